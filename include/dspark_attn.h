@@ -67,7 +67,8 @@ typedef enum {
     DSPARK_ERR_CUDA = 6,        /* a CUDA runtime call or launch failed */
     DSPARK_ERR_DEVICE = 7,      /* (device) a bounded wait gave up */
     DSPARK_ERR_ALIGN = 8,       /* a tensor pointer is not 16-byte aligned */
-    DSPARK_ERR_UNSUPPORTED = 9  /* sizes outside what the kernels implement */
+    DSPARK_ERR_UNSUPPORTED = 9, /* sizes outside what the kernels implement */
+    DSPARK_ERR_PAGE = 10        /* (device) a cache page, kv_len or q_start out of range (dspark_latent.h) */
 } dspark_status;
 
 typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
@@ -155,7 +156,8 @@ DSPARK_API dspark_status dspark_attn_bwd(const dspark_problem *p, const void *q,
                               void *workspace, size_t workspace_bytes, uint32_t flags, void *stream);
 
 /* Synchronises the stream, reads and clears the workspace error word.
- * Returns DSPARK_OK, DSPARK_ERR_ANCHOR (a kept anchor was out of range) or
+ * Returns DSPARK_OK, DSPARK_ERR_ANCHOR (a kept anchor was out of range),
+ * DSPARK_ERR_PAGE (a paged-cache argument was out of range) or
  * DSPARK_ERR_DEVICE (a bounded wait in a kernel gave up). */
 DSPARK_API dspark_status dspark_get_error(void *workspace, void *stream);
 

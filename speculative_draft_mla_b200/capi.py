@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in include/dspark_attn.h (argument marshalling only).
+"""Python binding of the C ABI in include/dspark_attn.h and include/dspark_latent.h (argument
+marshalling only).
 
 Every step of the attention runs in the CUDA library ``libdspark_attn.so``
 built in-tree by ``speculative_draft_mla_b200.build``. There is no fallback:
@@ -16,11 +17,14 @@ LIB_PATH = os.path.join(_HERE, "libdspark_attn.so")
 F32, BF16 = 0, 1
 FLAG_REUSE_DESCRIPTOR = 1
 STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_SHAPE", 3: "ERR_DTYPE", 4: "ERR_ANCHOR", 5: "ERR_WORKSPACE",
-          6: "ERR_CUDA", 7: "ERR_DEVICE", 8: "ERR_ALIGN", 9: "ERR_UNSUPPORTED"}
+          6: "ERR_CUDA", 7: "ERR_DEVICE", 8: "ERR_ALIGN", 9: "ERR_UNSUPPORTED", 10: "ERR_PAGE"}
 EXPORTS = ("dspark_workspace_size", "dspark_build_descriptor", "dspark_attn_fwd", "dspark_attn_bwd",
            "dspark_get_error", "dspark_status_string", "dspark_sample_anchors", "dspark_launch_counter",
            "dspark_set_wait_limit_ns", "dspark_sample_anchors_gpu", "dspark_build_draft_inputs",
-           "dspark_loss_workspace_size", "dspark_loss_fwd_bwd")
+           "dspark_loss_workspace_size", "dspark_loss_fwd_bwd", "dspark_latent_workspace_size",
+           "dspark_latent_attn_fwd", "dspark_latent_attn_bwd", "dspark_latent_row_bytes",
+           "dspark_latent_cache_write", "dspark_latent_cache_read", "dspark_latent_paged_workspace_size",
+           "dspark_latent_attn_paged")
 MASK_ID = 154821  # the page's MASK token id
 
 
@@ -29,6 +33,28 @@ class Problem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("n_h", ctypes.c_int32), ("S", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("W", ctypes.c_int32), ("d_c", ctypes.c_int32), ("d_r", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("rope_base", ctypes.c_double), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class LatentProblem(ctypes.Structure):
+    """Mirror of dspark_latent_problem."""
+    _fields_ = [("B", ctypes.c_int32), ("n_h", ctypes.c_int32), ("S", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("W", ctypes.c_int32), ("d_l", ctypes.c_int32), ("d_r", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("rope_base", ctypes.c_double), ("scale", ctypes.c_double), ("reserved", ctypes.c_int32 * 2)]
+
+
+class LatentCache(ctypes.Structure):
+    """Mirror of dspark_latent_cache."""
+    _fields_ = [("T", ctypes.c_int32), ("d_l", ctypes.c_int32), ("d_r", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class LatentPaged(ctypes.Structure):
+    """Mirror of dspark_latent_paged."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("n_seq", "T", "n_h", "d_l", "d_r", "page_size", "n_pages", "max_pages",
+                                              "max_kv_len", "window", "causal", "dtype", "kind", "reserved")] + \
+               [(f, ctypes.c_int64) for f in ("q_token_stride", "q_head_stride", "o_token_stride", "o_head_stride")] + \
+               [("rope_base", ctypes.c_double), ("scale", ctypes.c_double)]
 
 
 class DsparkError(RuntimeError):
@@ -76,6 +102,22 @@ def load():
     lib.dspark_loss_fwd_bwd.restype = ctypes.c_int
     lib.dspark_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.dspark_set_wait_limit_ns.restype = ctypes.c_uint64
+    lp, lc, lq = ctypes.POINTER(LatentProblem), ctypes.POINTER(LatentCache), ctypes.POINTER(LatentPaged)
+    f64 = ctypes.c_double
+    lib.dspark_latent_workspace_size.argtypes = [lp]
+    lib.dspark_latent_workspace_size.restype = sz
+    lib.dspark_latent_attn_fwd.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, sz, u32, vp]
+    lib.dspark_latent_attn_bwd.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, u32, vp]
+    lib.dspark_latent_row_bytes.argtypes = [i32, i32, i32]
+    lib.dspark_latent_row_bytes.restype = sz
+    lib.dspark_latent_cache_write.argtypes = [lc, vp, vp, vp, f64, f64, vp, vp, vp, vp]
+    lib.dspark_latent_cache_read.argtypes = [lc, vp, vp, vp, vp, vp]
+    lib.dspark_latent_paged_workspace_size.argtypes = [lq]
+    lib.dspark_latent_paged_workspace_size.restype = sz
+    lib.dspark_latent_attn_paged.argtypes = [lq, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for f in ("dspark_latent_attn_fwd", "dspark_latent_attn_bwd", "dspark_latent_cache_write",
+              "dspark_latent_cache_read", "dspark_latent_attn_paged"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("dspark_build_descriptor", "dspark_attn_fwd", "dspark_attn_bwd", "dspark_get_error"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
@@ -286,3 +328,216 @@ def sample_anchors(loss_mask, N, seed):
     if rc < 0:
         raise DsparkError(2, "dspark_sample_anchors")
     return anchors, keep
+
+
+# ---- latent space (include/dspark_latent.h) --------------------------------------------------
+CACHE_F32, CACHE_BF16, CACHE_FP8 = 0, 1, 2
+LATENT_SCALE = 256 ** -0.5  # of the page's expanded head, 192 + 64 wide
+
+
+def latent_problem(B, n_h, S, N, W, d_l=512, d_r=64, scale=LATENT_SCALE, rope_base=10000.0, dtype=BF16):
+    return LatentProblem(B, n_h, S, N, W, d_l, d_r, int(dtype), float(rope_base), float(scale), (0, 0))
+
+
+def latent_workspace_size(prob):
+    return int(load().dspark_latent_workspace_size(ctypes.byref(prob)))
+
+
+def alloc_latent_workspace(prob, device):
+    n = latent_workspace_size(prob)
+    if n == 0:
+        raise DsparkError(2, "latent_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _same(name, t, shape, dtype, device):
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, not %s" % (name, t.device, device))
+
+
+def _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base):
+    _cuda(q, c, kr, anchors, keep)
+    if q.dim() != 4 or c.dim() != 3 or kr.dim() != 3 or q.shape[2] % 5:
+        raise ValueError("q [B, n_h, 5N, d_l + d_r], c [B, S + 5N, d_l], kr [B, S + 5N, d_r]")
+    B, n_h, R, dk = q.shape
+    d_l, d_r = c.shape[2], kr.shape[2]
+    if dk != d_l + d_r:
+        raise ValueError("q is %d wide, c and kr %d + %d" % (dk, d_l, d_r))
+    _same("c", c, (B, S + R, d_l), q.dtype, q.device)
+    _same("kr", kr, (B, S + R, d_r), q.dtype, q.device)
+    _same("anchors", anchors, (B, R // 5), torch.int32, q.device)
+    _same("keep", keep, (B, R // 5), torch.uint8, q.device)
+    return latent_problem(B, n_h, S, R // 5, W, d_l, d_r, scale, rope_base, dtype_code(q.dtype))
+
+
+def latent_attn_fwd(q, c, kr, anchors, keep, S, W, scale=LATENT_SCALE, rope_base=10000.0, workspace=None, flags=0,
+                    out=None, stream=None):
+    """Draft attention over latents: q [B, n_h, 5N, d_l + d_r], c [B, S + 5N, d_l], kr [B, S + 5N, d_r].
+    Returns (o [B, n_h, 5N, d_l], lse, workspace). ``out`` may pass preallocated (o, lse)."""
+    prob = _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base)
+    if workspace is None:
+        workspace = alloc_latent_workspace(prob, q.device)
+    if out is None:
+        out = (torch.empty(q.shape[:3] + (c.shape[2],), dtype=q.dtype, device=q.device),
+               torch.empty(q.shape[:3], dtype=torch.float32, device=q.device))
+    o, lse = out
+    _cuda(o, lse, workspace)
+    _same("o", o, q.shape[:3] + (c.shape[2],), q.dtype, q.device)
+    _same("lse", lse, q.shape[:3], torch.float32, q.device)
+    with torch.cuda.device(q.device):
+        _check(load().dspark_latent_attn_fwd(ctypes.byref(prob), _ptr(q), _ptr(c), _ptr(kr), _ptr(anchors), _ptr(keep),
+                                             _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), flags,
+                                             _stream(stream, q.device)), "dspark_latent_attn_fwd")
+    return o, lse, workspace
+
+
+def latent_attn_bwd(q, c, kr, anchors, keep, lse, dout, S, W, scale=LATENT_SCALE, rope_base=10000.0, workspace=None,
+                    flags=0, out=None, stream=None):
+    """Returns (dq, dc, dkr) for dL/dO = dout and the forward's lse (its O is not needed). ``out`` may pass
+    preallocated gradients."""
+    prob = _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base)
+    if workspace is None:
+        workspace = alloc_latent_workspace(prob, q.device)
+    if out is None:
+        out = (torch.empty_like(q), torch.empty_like(c), torch.empty_like(kr))
+    dq, dc, dkr = out
+    _cuda(lse, dout, dq, dc, dkr, workspace)
+    _same("lse", lse, q.shape[:3], torch.float32, q.device)
+    _same("dout", dout, q.shape[:3] + (c.shape[2],), q.dtype, q.device)
+    for name, g, x in (("dq", dq, q), ("dc", dc, c), ("dkr", dkr, kr)):
+        _same(name, g, x.shape, q.dtype, q.device)
+    with torch.cuda.device(q.device):
+        _check(load().dspark_latent_attn_bwd(ctypes.byref(prob), _ptr(q), _ptr(c), _ptr(kr), _ptr(anchors), _ptr(keep),
+                                             _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dc), _ptr(dkr), _ptr(workspace),
+                                             workspace.numel(), flags, _stream(stream, q.device)),
+               "dspark_latent_attn_bwd")
+    return dq, dc, dkr
+
+
+def latent_row_bytes(kind, d_l, d_r):
+    return int(load().dspark_latent_row_bytes(int(kind), int(d_l), int(d_r)))
+
+
+def _cache_kind(cache, d_l, d_r):
+    """Kind of a cache tensor [n_pages, page_size, row]: float32 / bfloat16 rows of d_l + d_r values, or the
+    bytes (uint8) of the 8-bit kind."""
+    kinds = {torch.float32: CACHE_F32, torch.bfloat16: CACHE_BF16, torch.uint8: CACHE_FP8}
+    _cuda(cache)
+    if cache.dim() != 3 or cache.dtype not in kinds:
+        raise ValueError("cache must be [n_pages, page_size, row] of float32, bfloat16 or uint8 (the 8-bit kind)")
+    kind = kinds[cache.dtype]
+    if cache.shape[2] * cache.element_size() != latent_row_bytes(kind, d_l, d_r):
+        raise ValueError("cache rows of %d elements do not fit d_l = %d, d_r = %d" % (cache.shape[2], d_l, d_r))
+    return kind
+
+
+def latent_cache(n_pages, page_size, d_l=512, d_r=64, kind=CACHE_BF16, device="cuda"):
+    """A zeroed paged cache of the given kind."""
+    nb = latent_row_bytes(kind, d_l, d_r)
+    if nb == 0:
+        raise DsparkError(9, "latent_row_bytes")
+    dt = {CACHE_F32: torch.float32, CACHE_BF16: torch.bfloat16, CACHE_FP8: torch.uint8}[kind]
+    return torch.zeros(n_pages, page_size, nb // dt.itemsize, dtype=dt, device=device)
+
+
+def latent_cache_write(cache, c, kr, positions, slots, norm_weight=None, eps=1e-5, rope_base=10000.0, stream=None):
+    """Writes T tokens' latents c [T, d_l] (RMS-normed when norm_weight [d_l] is given) and rope keys kr [T, d_r]
+    (turned to positions [T] int32) into rows slots [T] int64 of the cache; a slot out of range writes nothing."""
+    _cuda(c, kr, positions, slots, norm_weight)
+    if c.dim() != 2 or kr.dim() != 2:
+        raise ValueError("c [T, d_l], kr [T, d_r]")
+    T, d_l = c.shape
+    kind = _cache_kind(cache, d_l, kr.shape[1])
+    dev = cache.device
+    _same("c", c, (T, d_l), c.dtype, dev)
+    _same("kr", kr, (T, kr.shape[1]), c.dtype, dev)
+    _same("positions", positions, (T,), torch.int32, dev)
+    _same("slots", slots, (T,), torch.int64, dev)
+    if norm_weight is not None:
+        _same("norm_weight", norm_weight, (d_l,), c.dtype, dev)
+    prob = LatentCache(T, d_l, kr.shape[1], kind, cache.shape[0], cache.shape[1], dtype_code(c.dtype), 0)
+    with torch.cuda.device(dev):
+        _check(load().dspark_latent_cache_write(ctypes.byref(prob), _ptr(c), _ptr(kr), _ptr(norm_weight), float(eps),
+                                                float(rope_base), _ptr(positions), _ptr(slots), _ptr(cache),
+                                                _stream(stream, dev)), "dspark_latent_cache_write")
+
+
+def latent_cache_read(cache, slots, d_l=512, d_r=64, dtype=torch.bfloat16, stream=None):
+    """Rows slots [T] int64 as the values that they stand for: (c [T, d_l], rotated rope keys [T, d_r])."""
+    kind = _cache_kind(cache, d_l, d_r)
+    _cuda(slots)
+    dev = cache.device
+    _same("slots", slots, (slots.numel(),), torch.int64, dev)
+    T = slots.numel()
+    c = torch.empty(T, d_l, dtype=dtype, device=dev)
+    kr = torch.empty(T, d_r, dtype=dtype, device=dev)
+    prob = LatentCache(T, d_l, d_r, kind, cache.shape[0], cache.shape[1], dtype_code(dtype), 0)
+    with torch.cuda.device(dev):
+        _check(load().dspark_latent_cache_read(ctypes.byref(prob), _ptr(cache), _ptr(slots), _ptr(c), _ptr(kr),
+                                               _stream(stream, dev)), "dspark_latent_cache_read")
+    return c, kr
+
+
+def _paged(q, cache, block_table, max_kv_len, d_l, d_r, scale, causal, window, rope_base, o=None):
+    kind = _cache_kind(cache, d_l, d_r)
+    if not q.is_cuda or q.dim() != 3 or q.shape[2] != d_l + d_r:
+        raise ValueError("q must be a CUDA tensor [T, n_h, d_l + d_r]")
+    for name, t in (("q", q), ("o", o)):
+        if t is not None and t.numel() and t.stride(2) != 1:
+            raise ValueError("%s must be contiguous in its last dimension" % name)
+    _cuda(block_table)
+    T, n_h = q.shape[:2]
+
+    def strides(t):
+        return (0, 0) if t is None or t.numel() == 0 else (t.stride(0), t.stride(1))
+
+    return LatentPaged(block_table.shape[0], T, n_h, d_l, d_r, cache.shape[1], cache.shape[0], block_table.shape[1],
+                       int(max_kv_len), int(window), int(bool(causal)), dtype_code(q.dtype), kind, 0, *strides(q),
+                       *strides(o), float(rope_base), float(scale))
+
+
+def latent_paged_workspace_size(prob):
+    return int(load().dspark_latent_paged_workspace_size(ctypes.byref(prob)))
+
+
+def alloc_latent_paged_workspace(q, cache, block_table, max_kv_len=0, d_l=512, d_r=64, window=0):
+    """Workspace of latent_attn_paged for these sizes (any mask)."""
+    prob = _paged(q, cache, block_table, max_kv_len, d_l, d_r, LATENT_SCALE, True, window, 10000.0)
+    n = latent_paged_workspace_size(prob)
+    if n == 0:
+        raise DsparkError(2, "latent_paged_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def latent_attn_paged(q, cache, block_table, q_start, kv_len, max_kv_len=0, d_l=512, d_r=64, scale=LATENT_SCALE,
+                      causal=True, window=0, rope_base=10000.0, workspace=None, out=None, stream=None):
+    """New tokens q [T, n_h, d_l + d_r] (token and head strides free) over a paged latent cache. q_start
+    [n_seq + 1], kv_len [n_seq] and block_table [n_seq, max_pages] int32. causal=False is a draft block whose
+    tokens see one another. Returns (o [T, n_h, d_l], lse [T, n_h], workspace); rows behind the last sequence are
+    left as they were in ``out`` and are unspecified otherwise."""
+    o, lse = out if out is not None else (None, None)
+    if o is None:
+        o = torch.empty(q.shape[0], q.shape[1], d_l, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
+    prob = _paged(q, cache, block_table, max_kv_len, d_l, d_r, scale, causal, window, rope_base, o)
+    _cuda(q_start, kv_len, lse)
+    n_seq, dev = block_table.shape[0], q.device
+    if cache.device != dev:
+        raise ValueError("cache is on %s, not %s" % (cache.device, dev))
+    _same("block_table", block_table, block_table.shape, torch.int32, dev)
+    _same("q_start", q_start, (n_seq + 1,), torch.int32, dev)
+    _same("kv_len", kv_len, (n_seq,), torch.int32, dev)
+    _same("o", o, (q.shape[0], q.shape[1], d_l), q.dtype, dev)
+    _same("lse", lse, q.shape[:2], torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(max(latent_paged_workspace_size(prob), 256), dtype=torch.uint8, device=dev)
+    _cuda(workspace)
+    with torch.cuda.device(dev):
+        _check(load().dspark_latent_attn_paged(ctypes.byref(prob), _ptr(q), _ptr(cache), _ptr(block_table),
+                                               _ptr(q_start), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(workspace),
+                                               workspace.numel(), _stream(stream, dev)), "dspark_latent_attn_paged")
+    return o, lse, workspace

@@ -6,6 +6,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "dspark_latent.cuh"
 #include "dspark_steps.cuh"
 
 using namespace dspark;
@@ -13,6 +14,7 @@ using namespace dspark;
 namespace dspark {
 static std::atomic<uint64_t> g_launches{0};
 static std::atomic<uint64_t> g_wait_ns{kWaitTimeoutNs};  // pipeline-wait limit of later launches
+uint64_t wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
 void count_launch(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 }  // namespace dspark
 
@@ -245,6 +247,7 @@ dspark_status dspark_get_error(void *workspace, void *stream) {
     }
     if (word & kErrTimeout) return DSPARK_ERR_DEVICE;
     if (word & kErrAnchor) return DSPARK_ERR_ANCHOR;
+    if (word & kErrPage) return DSPARK_ERR_PAGE;
     return DSPARK_OK;
 }
 
@@ -321,6 +324,7 @@ const char *dspark_status_string(dspark_status s) {
         case DSPARK_ERR_DEVICE: return "a bounded device-side wait gave up";
         case DSPARK_ERR_ALIGN: return "a tensor pointer is not 16-byte aligned";
         case DSPARK_ERR_UNSUPPORTED: return "sizes outside what the kernels implement";
+        case DSPARK_ERR_PAGE: return "a cache page, kv_len or q_start is out of range";
     }
     return "unknown status";
 }

@@ -15,28 +15,29 @@ constexpr uint32_t kErrPage = 4u;  // error word bit: a page, kv_len or q_start 
 // The Prob of dspark_internal.cuh with d_c = d_v = d_l, so that the mask
 // descriptor and the rope-key rotation serve this family too.
 struct LatWsLayout {
-    size_t err, cnt, sorted_n, sorted_a, rope, kr_rot;  // as WsLayout
+    size_t err, cnt, sorted_n, sorted_a, rope;  // as WsLayout
+    size_t kr;     // turned rope keys [B, L, d_r]: fp32 (CUDA-core kernels) or bf16 hi, then bf16 lo
     size_t fwd_total;
     size_t dvec;   // float [B, n_h, 5N]: D = sum_k P dP (CUDA-core backward)
     size_t dacc;   // float [B, L, d_l + d_r]: key gradients (tensor-core backward)
     size_t total;
 };
 
-bool lat_tc_supported(const Prob &p);
+bool lat_tc_supported(const Prob &p);      // the tensor-core forward takes the problem
+bool lat_bwd_tc_supported(const Prob &p);  // ... backward
 uint64_t wait_limit_ns();  // limit of the pipeline waits in effect (dspark_set_wait_limit_ns)
 
 inline LatWsLayout lat_layout(const Prob &p) {
     LatWsLayout w;
     size_t off = 0;
-    const size_t esz = p.dtype == DSPARK_BF16 ? 2 : 4;
     w.err = off;       off = align256(off + 256);
     w.cnt = off;       off = align256(off + sizeof(int32_t) * (size_t)p.B);
     w.sorted_n = off;  off = align256(off + sizeof(int32_t) * (size_t)p.B * p.N);
     w.sorted_a = off;  off = align256(off + sizeof(int32_t) * (size_t)p.B * p.N);
     w.rope = off;      off = align256(off + sizeof(float2) * (size_t)p.P * (p.d_r / 2));
-    w.kr_rot = off;    off = align256(off + esz * (size_t)p.B * p.L * p.d_r);
+    w.kr = off;        off = align256(off + 4 * (size_t)p.B * p.L * p.d_r);
     w.fwd_total = off;
-    const bool tc = lat_tc_supported(p);
+    const bool tc = lat_bwd_tc_supported(p);
     w.dvec = off;      off = align256(off + (tc ? 0 : sizeof(float) * (size_t)p.B * p.n_h * p.R));
     w.dacc = off;      off = align256(off + (tc ? sizeof(float) * (size_t)p.B * p.L * p.dqk : 0));
     w.total = off;
@@ -44,7 +45,9 @@ inline LatWsLayout lat_layout(const Prob &p) {
 }
 
 struct LatWs {
-    Ws base;  // err, sched, cnt, sorted_n, sorted_a, rope, kr_rot
+    Ws base;  // err, cnt, sorted_n, sorted_a, rope
+    float *kr_f32;
+    __nv_bfloat16 *kr_hi, *kr_lo;
     float *dvec, *dacc;
 };
 
@@ -53,17 +56,24 @@ inline LatWs lat_view(const Prob &p, void *ws) {
     char *c = (char *)ws;
     LatWs w{};
     w.base.err = (uint32_t *)(c + l.err);
-    w.base.sched = (int32_t *)(c + l.err + 128);
     w.base.cnt = (int32_t *)(c + l.cnt);
     w.base.sorted_n = (int32_t *)(c + l.sorted_n);
     w.base.sorted_a = (int32_t *)(c + l.sorted_a);
     w.base.rope = (float2 *)(c + l.rope);
-    w.base.kr_rot = (void *)(c + l.kr_rot);
+    w.kr_f32 = (float *)(c + l.kr);
+    w.kr_hi = (__nv_bfloat16 *)(c + l.kr);
+    w.kr_lo = w.kr_hi + (size_t)p.B * p.L * p.d_r;
     w.dvec = (float *)(c + l.dvec);
     w.dacc = (float *)(c + l.dacc);
     return w;
 }
 
+// turned rope keys; with pad != NULL, the padding blocks' rows too (t[0] per
+// head, t[1] and t[2] shared by the heads)
+cudaError_t launch_lat_prep(const Prob &p, const void *kr, const int32_t *anchors, const uint8_t *keep,
+                            const PadRows *pad, bool tc, const LatWs &ws, cudaStream_t st);
+cudaError_t launch_lat_fwd_tc(const Prob &p, const void *q, const void *c, void *o, float *lse, const LatWs &ws,
+                              cudaStream_t st);
 cudaError_t launch_lat_fwd_simt(const Prob &p, const void *q, const void *c, const int32_t *anchors,
                                 const uint8_t *keep, void *o, float *lse, const LatWs &ws, cudaStream_t st);
 cudaError_t launch_lat_bwd_simt(const Prob &p, const void *q, const void *c, const int32_t *anchors,

@@ -170,8 +170,17 @@ dspark_status dspark_latent_attn_fwd(const dspark_latent_problem *pp, const void
     cudaStream_t st = (cudaStream_t)stream;
     const LatWs w = lat_view(p, workspace);
     if (!(flags & DSPARK_FLAG_REUSE_DESCRIPTOR)) DSPARK_CUDA(launch_build_descriptor(p, anchors, keep, w.base, st));
-    DSPARK_CUDA(launch_rotate_kr(p, kr, anchors, keep, nullptr, w.base, st));
-    DSPARK_CUDA(launch_lat_fwd_simt(p, q, c, anchors, keep, o, lse, w, st));
+    const bool tc = lat_tc_supported(p);
+    PadRows pad{};  // the tensor-core kernel leaves padding blocks' rows to the preparation
+    pad.t[0] = o;
+    pad.rows[0] = p.R;
+    pad.width[0] = p.d_c;
+    pad.lse = lse;
+    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, tc ? &pad : nullptr, tc, w, st));
+    if (tc)
+        DSPARK_CUDA(launch_lat_fwd_tc(p, q, c, o, lse, w, st));
+    else
+        DSPARK_CUDA(launch_lat_fwd_simt(p, q, c, anchors, keep, o, lse, w, st));
     return DSPARK_OK;
 }
 
@@ -190,7 +199,7 @@ dspark_status dspark_latent_attn_bwd(const dspark_latent_problem *pp, const void
     cudaStream_t st = (cudaStream_t)stream;
     const LatWs w = lat_view(p, workspace);
     if (!(flags & DSPARK_FLAG_REUSE_DESCRIPTOR)) DSPARK_CUDA(launch_build_descriptor(p, anchors, keep, w.base, st));
-    DSPARK_CUDA(launch_rotate_kr(p, kr, anchors, keep, nullptr, w.base, st));
+    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, nullptr, false, w, st));
     DSPARK_CUDA(launch_lat_bwd_simt(p, q, c, anchors, keep, lse, do_, dq, dc, dkr, w, st));
     return DSPARK_OK;
 }

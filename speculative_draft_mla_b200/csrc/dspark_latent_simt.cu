@@ -46,10 +46,11 @@ __device__ __forceinline__ bool live_block(const Prob &p, const int32_t *anchors
 
 // Keys of the training layout: element d of key position k of batch row b.
 template <typename T> struct DenseKeys {
-    const T *c, *krr;
+    const T *c;
+    const float *krr;  // turned, fp32
     int d_l, d_r;
     __device__ __forceinline__ float at(size_t pos, int d) const {
-        return d < d_l ? to_f(c[pos * d_l + d]) : (d < d_l + d_r ? to_f(krr[pos * d_r + d - d_l]) : 0.f);
+        return d < d_l ? to_f(c[pos * d_l + d]) : (d < d_l + d_r ? krr[pos * d_r + d - d_l] : 0.f);
     }
 };
 
@@ -57,7 +58,7 @@ template <typename T> struct DenseKeys {
 // Forward, one warp per row: online softmax over four keys a step.
 template <typename T, int NL>
 __global__ void __launch_bounds__(kWarps * 32) k_lat_fwd_simt(Prob p, const T *__restrict__ q,
-                                                              const T *__restrict__ c, const T *__restrict__ krr,
+                                                              const T *__restrict__ c, const float *__restrict__ krr,
                                                               const int32_t *__restrict__ anchors,
                                                               const uint8_t *__restrict__ keep,
                                                               const float2 *__restrict__ tab, T *__restrict__ o,
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lat_fwd_simt(Prob p, const T *_
 // pass over the keys for D, a second one for dq = sum_k dS_k k.
 template <typename T, int NL>
 __global__ void __launch_bounds__(kWarps * 32) k_lat_bwd_q_simt(Prob p, const T *__restrict__ q,
-                                                                const T *__restrict__ c, const T *__restrict__ krr,
+                                                                const T *__restrict__ c, const float *__restrict__ krr,
                                                                 const int32_t *__restrict__ anchors,
                                                                 const uint8_t *__restrict__ keep,
                                                                 const float2 *__restrict__ tab,
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lat_bwd_q_simt(Prob p, const T 
 // of its own block for a draft key) and are summed in a fixed order.
 template <typename T, int NL>
 __global__ void __launch_bounds__(kWarps * 32) k_lat_bwd_k_simt(Prob p, const T *__restrict__ q,
-                                                                const T *__restrict__ c, const T *__restrict__ krr,
+                                                                const T *__restrict__ c, const float *__restrict__ krr,
                                                                 const int32_t *__restrict__ anchors,
                                                                 const uint8_t *__restrict__ keep,
                                                                 const float2 *__restrict__ tab,
@@ -410,7 +411,7 @@ cudaError_t fwd_t(const Prob &p, const void *q, const void *c, const int32_t *an
     if (rows == 0) return cudaSuccess;
     count_launch();
     k_lat_fwd_simt<T, NL><<<(unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
-        p, (const T *)q, (const T *)c, (const T *)ws.base.kr_rot, anchors, keep, ws.base.rope, (T *)o, lse);
+        p, (const T *)q, (const T *)c, ws.kr_f32, anchors, keep, ws.base.rope, (T *)o, lse);
     return cudaGetLastError();
 }
 
@@ -422,13 +423,13 @@ cudaError_t bwd_t(const Prob &p, const void *q, const void *c, const int32_t *an
     if (rows) {
         count_launch();
         k_lat_bwd_q_simt<T, NL><<<(unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
-            p, (const T *)q, (const T *)c, (const T *)ws.base.kr_rot, anchors, keep, ws.base.rope, lse,
+            p, (const T *)q, (const T *)c, ws.kr_f32, anchors, keep, ws.base.rope, lse,
             (const T *)dout, (T *)dq, ws.dvec);
     }
     if (p.B) {
         count_launch();
         k_lat_bwd_k_simt<T, NL><<<dim3(p.L, p.B), kWarps * 32, sizeof(float) * kWarps * p.dqk, st>>>(
-            p, (const T *)q, (const T *)c, (const T *)ws.base.kr_rot, anchors, keep, ws.base.rope, lse,
+            p, (const T *)q, (const T *)c, ws.kr_f32, anchors, keep, ws.base.rope, lse,
             (const T *)dout, ws.dvec, (T *)dc, (T *)dkr);
     }
     return cudaGetLastError();
@@ -446,7 +447,7 @@ template <typename T, int KIND> cudaError_t paged_t(const Paged &p, cudaStream_t
 
 }  // namespace
 
-bool lat_tc_supported(const Prob &p) { return false; }
+bool lat_bwd_tc_supported(const Prob &p) { return false; }
 
 cudaError_t launch_lat_fwd_simt(const Prob &p, const void *q, const void *c, const int32_t *anchors,
                                 const uint8_t *keep, void *o, float *lse, const LatWs &ws, cudaStream_t st) {

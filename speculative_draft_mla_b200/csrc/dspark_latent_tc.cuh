@@ -1,0 +1,101 @@
+// Helpers of the latent-space tensor-core kernels beside dspark_tc_common.cuh.
+#pragma once
+
+#include "dspark_latent.cuh"
+#include "dspark_tc_common.cuh"
+
+namespace dspark {
+namespace tc {
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// 4-D tiled TMA load (no multicast) completing on bar's transaction count.
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, uint64_t *bar, int x, int y, int z,
+                                            int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"((uint64_t)m), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+// 32 bytes to global memory: one store where the address allows it.
+__device__ __forceinline__ void st_global_32B(void *p, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+// x = hi + lo, both bf16, to 2^-17 of x; pairs packed low half first. An
+// infinity has no remainder.
+__device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16x2(x0, x1);
+    const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
+    lo = pack_bf16x2(fabsf(h0) <= 3.4e38f ? x0 - h0 : 0.f, fabsf(h1) <= 3.4e38f ? x1 - h1 : 0.f);
+}
+
+// bf16 tensor map of up to 4 dimensions (strides in bytes, of dimensions 1 ..),
+// 128-byte swizzle; box[0] = 64 elements.
+inline bool make_map_nd(CUtensorMap *m, const void *base, int nd, const uint64_t *dims, const uint64_t *strides,
+                        const uint32_t *box) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[4], s[3];
+    cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < nd; i++) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i) s[i - 1] = strides[i - 1];
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, nd, const_cast<void *>(base), d, s, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tc
+
+// ---- work items of the draft kernels -------------------------------------------
+// Item w is a kept block (batch rows in order, blocks by anchor) and one of
+// nsplit runs of its tiles of heads.
+struct DraftItem {
+    int b, n, a, t0, t1;
+};
+struct DraftCursor {
+    const int32_t *cnt, *sorted_n, *sorted_a;
+    int B, N, nsplit, tiles, per;  // per: tiles in a run
+    int b = 0, base = 0;           // batch row, kept blocks before it
+    __device__ __forceinline__ bool at(int w, DraftItem &it) {  // w must not go down
+        const int blk = w / nsplit, part = w % nsplit;
+        while (b < B) {
+            const int c = cnt[b];
+            if (blk < base + c) break;
+            base += c;
+            b++;
+        }
+        if (b >= B) return false;
+        const size_t i = (size_t)b * N + (blk - base);
+        it.b = b;
+        it.n = sorted_n[i];
+        it.a = sorted_a[i];
+        it.t0 = part * per;
+        it.t1 = min(tiles, it.t0 + per);
+        return true;
+    }
+};
+
+}  // namespace dspark

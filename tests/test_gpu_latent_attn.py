@@ -74,6 +74,8 @@ CASES = {
     "page_64_heads": (1, 260, 6, 128, 64, 512, 64, 1.0),
     "page_70_heads_window_two": (1, 90, 2, 2, 70, 512, 64, 1.0),
     "page_window_17": (3, 70, 5, 17, 6, 512, 64, 0.8),
+    # more blocks than SMs: several blocks and tiles in turn on one SM
+    "page_200_blocks": (1, 210, 200, 24, 30, 512, 64, 1.0),
     "page_window_129": (1, 300, 3, 129, 4, 512, 64, 1.0),
     "page_window_wider_than_context": (1, 40, 4, 128, 8, 512, 64, 1.0),
 }

@@ -114,7 +114,7 @@ struct Paged {
 };
 
 size_t paged_workspace_size(const Paged &p);
-cudaError_t launch_paged(const Paged &p, void *ws, cudaStream_t st);
+cudaError_t launch_paged(const Paged &p, void *ws, cudaStream_t st);  // plan and attention
 
 #ifdef __CUDACC__
 // cos and sin of pos * f: the angle formed in 64 bits and brought into

@@ -1,50 +1,173 @@
-// Attention of new tokens over the paged latent cache: dispatch.
-#include "dspark_latent.cuh"
+// Attention of new tokens over the paged latent cache: the plan of a call and
+// the choice of kernels.
+#include <algorithm>
+
+#include "dspark_latent_paged.cuh"
 
 namespace dspark {
 
-cudaError_t launch_paged_simt(const Paged &p, cudaStream_t st);
-
 namespace {
 
-// Clears the error word, then sets the page bit for what only the device can
-// see: sequence bounds and the pages that the sequences' keys lie in.
-__global__ void k_paged_check(const Paged p) {
-    __shared__ int bad;
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
-    bool mine = false;
-    for (int s = threadIdx.x >> 5; s < p.n_seq; s += blockDim.x >> 5) {
-        const SeqView v = seq_view(p, s);
-        mine |= v.bad;
-        if (v.q_len == 0) continue;
-        // the pages some row of the sequence reads
-        int lo, hi, l1, h1;
-        seq_range(p, v, 0, &lo, &h1);
-        seq_range(p, v, v.q_len - 1, &l1, &hi);
-        if (hi <= lo) continue;
-        for (int g = lo / p.page_size + (threadIdx.x & 31); g <= (hi - 1) / p.page_size; g += 32) {
-            const int page = p.table[(size_t)s * p.max_pages + g];
-            mine |= page < 0 || page >= p.n_pages;
+// One launch ahead of the attention. CTA 0 writes the error word (the page bit
+// for a q_start or kv_len out of range, else 0; pages are checked by the
+// kernels that read them) and, for the tensor-core kernel, the list of row
+// tiles: tile r is up to 128 (token, head) rows of one sequence and takes
+// start[r + 1] - start[r] steps of 64 keys, at least one. The CTA pairs of the
+// attention share all steps evenly, wherever tiles begin and end; first[i] is
+// the tile that pair i begins in. The other CTAs fill the tokens' (cos, sin).
+__global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedPlan w, int tc, int tab_ctas) {
+    pdl_wait();
+    pdl_trigger();
+    if (blockIdx.x > 0) {
+        // one warp per token: its sequence by a search over the starts, 32 at a time
+        const int lane = threadIdx.x & 31;
+        for (int tok = (blockIdx.x - 1) * 32 + (threadIdx.x >> 5); tok < p.T; tok += tab_ctas * 32) {
+            int s = -1;
+            for (int s0 = 0; s0 < p.n_seq && s < 0; s0 += 32) {
+                bool mine = false;
+                if (s0 + lane < p.n_seq) {
+                    const SeqView v = seq_view(p, s0 + lane);
+                    mine = tok >= v.q0 && tok < v.q0 + v.q_len;
+                }
+                const unsigned any = __ballot_sync(0xffffffffu, mine);
+                if (any) s = s0 + __ffs(any) - 1;
+            }
+            if (s < 0) continue;
+            const SeqView v = seq_view(p, s);
+            w.tab[(size_t)tok * 32 + lane] = rope_cs(v.kv - v.q_len + tok - v.q0, p.freq.f[lane]);
         }
+        return;
     }
-    if (mine) bad = 1;
+    __shared__ long long wsteps[32], carry_steps;
+    __shared__ int wtiles[32], carry_tiles, bad;
+    if (threadIdx.x == 0) {
+        bad = 0;
+        carry_steps = 0;
+        carry_tiles = 0;
+    }
     __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int s0 = 0; s0 < p.n_seq; s0 += blockDim.x) {
+        const int s = s0 + threadIdx.x;
+        SeqView v{};
+        int nt = 0;
+        long long ns = 0;
+        if (s < p.n_seq) {
+            v = seq_view(p, s);
+            if (v.bad) bad = 1;
+            if (tc) {
+                nt = (v.q_len + w.tpt - 1) / w.tpt;
+                for (int t = 0; t < nt; t++) ns += tile_steps(p, v, t * w.tpt, min(v.q_len, (t + 1) * w.tpt));
+                nt *= w.hchunks;
+                ns *= w.hchunks;
+            }
+        }
+        if (!tc) continue;
+        // inclusive sums over the block
+        int it = nt;
+        long long is = ns;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, it, o);
+            const long long b = __shfl_up_sync(0xffffffffu, is, o);
+            if (lane >= o) {
+                it += a;
+                is += b;
+            }
+        }
+        if (lane == 31) {
+            wtiles[warp] = it;
+            wsteps[warp] = is;
+        }
+        __syncthreads();
+        int bt = carry_tiles + it - nt;
+        long long bs = carry_steps + is - ns;
+        for (int k = 0; k < warp; k++) {
+            bt += wtiles[k];
+            bs += wsteps[k];
+        }
+        __syncthreads();
+        if (threadIdx.x == blockDim.x - 1) {
+            carry_tiles = bt + nt;
+            carry_steps = bs + ns;
+        }
+        for (int t = 0; t < nt; t++) {
+            const int hc = t % w.hchunks, i0 = t / w.hchunks * w.tpt;
+            // (sequences that overlap, an error, could need more tiles than there is room for)
+            if (bt + t >= w.max_tiles) {
+                bad = 1;
+                break;
+            }
+            w.tiles[bt + t] = make_int4(s, i0, hc, 0);
+            w.start[bt + t] = bs;
+            bs += tile_steps(p, v, i0, min(v.q_len, i0 + w.tpt));
+        }
+        __syncthreads();
+    }
+    __syncthreads();
+    if (tc) {
+        const int n = min(carry_tiles, w.max_tiles);
+        long long total = carry_steps;
+        if (carry_tiles > w.max_tiles) total = 0;  // overlapping sequences: nothing is attended
+        const long long X = (total + kPairs - 1) / kPairs;
+        if (threadIdx.x == 0) {
+            w.head->total = total;
+            w.head->per = X;
+            w.start[total ? n : 0] = total;
+        }
+        __syncthreads();
+        if (total)
+            for (int r = threadIdx.x; r < n; r += blockDim.x) {
+                const long long a = w.start[r], b = w.start[r + 1];
+                for (long long i = (a + X - 1) / X; i < kPairs && i * X < b; i++) w.first[i] = r;
+            }
+    }
     if (threadIdx.x == 0) *p.err = bad ? kErrPage : 0u;
 }
 
 }  // namespace
 
-size_t paged_workspace_size(const Paged &p) { return 256; }
+bool paged_tc_supported(const Paged &p) {
+    return p.d_l == 512 && p.d_r == 64 && (p.kind == DSPARK_CACHE_BF16 || p.kind == DSPARK_CACHE_FP8);
+}
+
+size_t paged_layout(const Paged &p, void *ws, PagedPlan *w) {
+    PagedPlan r{};
+    char *c = (char *)ws;
+    size_t off = 256;
+    const bool tc = paged_tc_supported(p);
+    r.head = (PagedHead *)(c + 128);
+    r.tpt = p.n_h <= 128 ? 128 / p.n_h : 1;
+    r.hchunks = (p.n_h + 127) / 128;
+    r.max_tiles = tc ? (int)std::min<long long>(((long long)p.T / r.tpt + p.n_seq) * r.hchunks, 1ll << 30) : 0;
+    auto take = [&](size_t n) {
+        char *at = c + off;
+        off = align256(off + (tc ? n : 0));
+        return (void *)at;
+    };
+    r.first = (int *)take(sizeof(int) * kPairs);
+    r.tiles = (int4 *)take(sizeof(int4) * ((size_t)r.max_tiles + 1));
+    r.start = (long long *)take(sizeof(long long) * ((size_t)r.max_tiles + 1));
+    r.tab = (float2 *)take(sizeof(float2) * 32 * (size_t)p.T);
+    r.part_lse = (float *)take(sizeof(float) * 2 * kPairs * 128);
+    r.part_o = (float *)take(sizeof(float) * 2 * kPairs * 128 * 512);
+    if (w) *w = r;
+    return off;
+}
+
+size_t paged_workspace_size(const Paged &p) { return paged_layout(p, nullptr, nullptr); }
 
 cudaError_t launch_paged(const Paged &pp, void *ws, cudaStream_t st) {
     Paged p = pp;
     p.err = (uint32_t *)ws;
+    PagedPlan w;
+    paged_layout(p, ws, &w);
+    const bool run = p.T > 0 && p.n_seq > 0, tc = run && paged_tc_supported(p);
+    const int tab_ctas = tc ? std::min((p.T + 31) / 32, 296) : 0;
     count_launch();
-    k_paged_check<<<1, 1024, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.T == 0 || p.n_seq == 0) return e;
-    return launch_paged_simt(p, st);
+    cudaError_t e = launch_pdl(k_paged_plan, dim3(1 + tab_ctas), dim3(1024), 0, st, p, w, tc ? 1 : 0, tab_ctas);
+    if (e != cudaSuccess || !run) return e;
+    return tc ? launch_paged_tc(p, w, st) : launch_paged_simt(p, st);
 }
 
 }  // namespace dspark

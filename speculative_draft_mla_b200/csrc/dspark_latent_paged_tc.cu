@@ -1,0 +1,638 @@
+// Tensor-core attention of new tokens over the paged latent cache (512-wide
+// latents, 64-wide rope keys; bf16 and 8-bit rows), any length and mask.
+//
+// Row tile: 128 (token, head) rows of one sequence, which share the keys. The
+// fp32 output of 128 rows x 512 values would fill tensor memory by itself, so
+// two CTAs (a pair) take 256 value columns each and both form the scores: 1.5
+// times the tensor work of one, but no exchange, and the second read of a key
+// comes from L2. The steps (64 keys of a tile) of all tiles are one list that
+// the 74 pairs share evenly, wherever tiles begin and end; a tile that several
+// pairs work on leaves partial results (output and log-sum-exp, fp32), which
+// the last launch joins. So one token over a long context and a batch of ragged
+// chunks keep all SMs equally busy.
+//
+// Step: S = Q K^T (128 x 64) in TMEM; softmax with a running maximum (the
+// output is rescaled only when it grows by more than 2^8); P, bf16, through
+// shared memory; O += P V, V the same key rows read MN-major. Keys are gathered
+// row by row from their pages, so a page may end anywhere; slots of keys that
+// no row of the tile sees are zero, and a row's weight of a key outside its own
+// range is zero. 8-bit rows become bf16 on the way (exact: a scale is a power
+// of two).
+//
+// What bounds it: long contexts, the keys' way from L2 (74 KB a step and CTA,
+// twice the cache's bytes over all) and the tensor work of 1000 cycles a step;
+// few keys, latency of the launches and of a step.
+//
+// The query's turned rope slice is split as hi + lo of two bf16 (the cache's
+// rope keys are exact bf16 operands), so scores and LSE keep 2^-16.
+//
+// TMEM: O 0..255, S 256..319, Q 320..511 (latent slices 0 - 3, rope hi, rope
+// lo). Shared: Q slices 4 - 7, two key stages, P.
+// Warps: 0-7 softmax (warps w and w + 4 share 32 rows and take 32 keys and 128
+// output columns each), 8-11 Q, 12-15 and 16-19 keys of even and odd steps, 20
+// MMA issue. Every wait is bounded.
+#include <algorithm>
+
+#include "dspark_latent_paged.cuh"
+#include "dspark_latent_tc.cuh"
+
+namespace dspark {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kDL = 512, kDR = 64;
+constexpr int kKSlice = kStepKeys * 128, kStage = 9 * kKSlice;
+constexpr int oQ = 2 * kStage, oP = oQ + 4 * 128 * 128;
+constexpr int oX = oP + 128 * 128;  // pair exchange [2][2][128]: maximum of a step, row sums of a segment
+constexpr int oBar = oX + 4 * 512;
+constexpr int kSmem = oBar + 256;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320, kColR = kColQ + 4 * 32;
+constexpr int kSoft = 8, kWarpQ = 8, kWarpKeys = 12, kWarpM = 20;
+constexpr int kThreads = 21 * 32;
+constexpr float kGrow = 8.0f;  // log2 units
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A part of a tile that a pair works on: steps [s0, s1) of it.
+struct Seg {
+    int seq, i0, n_tok, hc;     // tokens i0 .. i0 + n_tok of the sequence
+    int tok0, kv, q_len, lo, hi;  // first token of q; keys; the tile's key range
+    int s0, s1, slot;           // slot >= 0: a partial result
+};
+struct SegCursor {
+    long long at, end, per;
+    int r, pair;
+    __device__ __forceinline__ void begin(const PagedPlan &w) {
+        pair = blockIdx.x >> 1;
+        per = w.head->per;
+        at = per * pair;
+        end = min(at + per, w.head->total);
+        r = at < end ? w.first[pair] : 0;
+    }
+    __device__ __forceinline__ bool next(const Paged &p, const PagedPlan &w, Seg &g) {
+        if (at >= end) return false;
+        const int4 t = w.tiles[r];
+        const long long a = w.start[r], b = w.start[r + 1];
+        const SeqView v = seq_view(p, t.x);
+        g.seq = t.x;
+        g.i0 = t.y;
+        g.hc = t.z;
+        g.n_tok = min(w.tpt, v.q_len - t.y);
+        g.tok0 = v.q0 + t.y;
+        g.kv = v.kv;
+        g.q_len = v.q_len;
+        tile_range(p, v, g.i0, g.i0 + g.n_tok, &g.lo, &g.hi);
+        g.s0 = (int)(at - a);
+        const long long e = min(end, b);
+        g.s1 = (int)(e - a);
+        g.slot = g.s0 == 0 && e == b ? -1 : 2 * pair + (g.s0 == 0 ? 1 : 0);
+        at = e;
+        r++;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Two e4m3 codes (low half of w) times s as a bf16 pair.
+__device__ __forceinline__ uint32_t fp8x2_bf16(uint32_t w, float s) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16x2(f.x * s, f.y * s);
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const PagedPlan w) {
+    extern __shared__ __align__(1024) uint8_t sm[];  // swizzle atoms: no room for slack
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + 2;
+    uint64_t *sfull = kempty + 2, *sfree = sfull + 1, *pready = sfull + 2, *pvdone = sfull + 3;
+    uint64_t *qready = sfull + 4, *qfree = sfull + 5, *ofree = sfull + 6, *drain = sfull + 7;
+    uint64_t *xbar = sfull + 8, *lbar = xbar + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lbar + 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(lbar + 5);
+    volatile uint16_t *kmask = reinterpret_cast<volatile uint16_t *>(lbar + 6);  // [2][4]: the stage's valid keys
+    float *xm = reinterpret_cast<float *>(sm + oX);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = blockIdx.x & 1;
+    const uint64_t wlim = p.wait_ns;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&kfull[i], 4);
+            mbar_init(&kempty[i], 1);
+        }
+        mbar_init(sfull, 1);
+        mbar_init(sfree, kSoft);
+        mbar_init(pready, kSoft);
+        mbar_init(pvdone, 1);
+        mbar_init(qready, 4);
+        mbar_init(qfree, 1);
+        mbar_init(ofree, kSoft);
+        mbar_init(drain, 1);
+        for (int i = 0; i < 8; i++) mbar_init(&xbar[i], 2);
+        for (int i = 0; i < 4; i++) mbar_init(&lbar[i], 2);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpM) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    SegCursor cur;
+    cur.begin(w);
+    Seg sg;
+
+    if (warp >= kWarpKeys && warp < kWarpM) {
+        // ------------------------------------------------ keys -> stages
+        const int gp = (warp - kWarpKeys) >> 2, wr = (warp - kWarpKeys) & 3;  // stage; 16 rows from 16 wr
+        const uint32_t stage = smem_u32(sm) + gp * kStage;
+        uint32_t g = 0;
+        bool ok = true;
+        while (ok && cur.next(p, w, sg))
+            for (int t = sg.s0; ok && t < sg.s1; t++, g++) {
+                if ((int)(g & 1) != gp) continue;
+                // lane l < 16: the slot of key 16 wr + l of the step
+                const int key = sg.lo + t * kStepKeys + 16 * wr + (lane & 15);
+                long long slot = -1;
+                if (key < sg.hi) {
+                    slot = key_slot(p, sg.seq, key);
+                    if (slot < 0 && lane < 16) atomicOr(p.err, kErrPage);
+                }
+                const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0) & 0xffffu;
+                if (g >= 2) ok = warp_all(mbar_wait(&kempty[gp], ((g >> 1) - 1) & 1, abort_flag, wlim));
+                if (!ok) break;
+                if (lane == 0) kmask[gp * 4 + wr] = (uint16_t)valid;
+                const uint8_t *cache = (const uint8_t *)p.cache;
+                const long long off = slot >= 0 ? slot * (long long)p.row_bytes : -1;
+                if constexpr (KIND == DSPARK_CACHE_BF16) {
+#pragma unroll 6
+                    for (int i = 0; i < 36; i++) {
+                        const int e = lane + 32 * i, row = e / 72, ch = e % 72;
+                        const long long o = __shfl_sync(0xffffffffu, off, row);
+                        cp16(stage + (ch >> 3) * kKSlice + sw128(16 * wr + row, ch & 7), cache + (o >= 0 ? o + ch * 16 : 0),
+                             o >= 0);
+                    }
+                } else {
+                    // lane: rows 8 rb + lane / 4, 16 codes of each slice; the rope slice as it is
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int row = 4 * i + (lane >> 3), ch = lane & 7;
+                        const long long o = __shfl_sync(0xffffffffu, off, row);
+                        cp16(stage + 8 * kKSlice + sw128(16 * wr + row, ch), cache + (o >= 0 ? o + kDL + ch * 16 : 0),
+                             o >= 0);
+                    }
+                    uint4 x[2][8];
+                    float4 sc[2];
+#pragma unroll
+                    for (int rb = 0; rb < 2; rb++) {
+                        const long long o = __shfl_sync(0xffffffffu, off, 8 * rb + (lane >> 2));
+                        const uint8_t *row = cache + (o >= 0 ? o : 0);
+                        sc[rb] = o >= 0 ? __ldg(reinterpret_cast<const float4 *>(row + kDL + 2 * kDR))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int s = 0; s < 8; s++)
+                            x[rb][s] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * s + 16 * (lane & 3)))
+                                              : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int rb = 0; rb < 2; rb++) {
+                        const int row = 16 * wr + 8 * rb + (lane >> 2);
+#pragma unroll
+                        for (int s = 0; s < 8; s++) {
+                            const float f = s < 2 ? sc[rb].x : s < 4 ? sc[rb].y : s < 6 ? sc[rb].z : sc[rb].w;
+                            const uint4 v = x[rb][s];
+                            uint8_t *dst = sm + gp * kStage + s * kKSlice;
+                            *reinterpret_cast<uint4 *>(dst + sw128(row, 2 * (lane & 3))) =
+                                make_uint4(fp8x2_bf16(v.x, f), fp8x2_bf16(v.x >> 16, f), fp8x2_bf16(v.y, f),
+                                           fp8x2_bf16(v.y >> 16, f));
+                            *reinterpret_cast<uint4 *>(dst + sw128(row, 2 * (lane & 3) + 1)) =
+                                make_uint4(fp8x2_bf16(v.z, f), fp8x2_bf16(v.z >> 16, f), fp8x2_bf16(v.w, f),
+                                           fp8x2_bf16(v.w >> 16, f));
+                        }
+                    }
+                }
+                cp_wait_all();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kfull[gp]);
+            }
+        cp_wait_all();
+    } else if (warp >= kWarpQ && warp < kWarpKeys) {
+        // -------------------------------------- Q -> shared and tensor memory
+        const int r = (warp - kWarpQ) * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)((warp - kWarpQ) * 32) << 16);
+        uint32_t k = 0;  // segments
+        bool ok = true;
+        for (; ok && cur.next(p, w, sg); k++) {
+            const int ti = w.tpt > 1 || p.n_h == 128 ? r / p.n_h : 0, h = sg.hc * 128 + r - ti * p.n_h;
+            const bool live = ti < sg.n_tok && h < p.n_h && (ti == 0 || w.hchunks == 1);
+            const int tok = sg.tok0 + (live ? ti : 0);
+            const __nv_bfloat16 *row = (const __nv_bfloat16 *)p.q + (long long)tok * p.q_ts + (live ? h : 0) * p.q_hs;
+            const uint4 *src = reinterpret_cast<const uint4 *>(row);
+            if (k > 0) {
+                if (live)
+                    for (int i = 0; i < 9; i++) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * i));
+                ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < 32; c++)
+                cp16(smem_u32(sm) + oQ + (c >> 3) * 16384 + sw128(r, c & 7), src + 32 + c, live);
+            tc_fence_after();
+            uint32_t x[32], lo[32];
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
+#pragma unroll
+                for (int u = 0; u < 8; u++) {
+                    const uint4 v = live ? __ldg(src + 8 * c + u) : make_uint4(0, 0, 0, 0);
+                    x[4 * u] = v.x;
+                    x[4 * u + 1] = v.y;
+                    x[4 * u + 2] = v.z;
+                    x[4 * u + 3] = v.w;
+                }
+                tmem_st32u(trow + kColQ + 32 * c, x);
+            }
+            const float4 *tab = reinterpret_cast<const float4 *>(w.tab + (size_t)tok * 32);
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const uint4 v = live ? __ldg(src + kDL / 8 + u) : make_uint4(0, 0, 0, 0);
+                const float4 c0 = __ldg(tab + 2 * u), c1 = __ldg(tab + 2 * u + 1);
+                const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+                const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float a = __uint_as_float(wv[i] << 16), b = __uint_as_float(wv[i] & 0xffff0000u);
+                    split_bf16x2(a * cs[i].x - b * cs[i].y, a * cs[i].y + b * cs[i].x, x[4 * u + i], lo[4 * u + i]);
+                }
+            }
+            tmem_st32u(trow + kColR, x);
+            tmem_st32u(trow + kColR + 32, lo);
+            tmem_wait_st();
+            tc_fence_before();
+            cp_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qready);
+        }
+        cp_wait_all();
+    } else if (warp == kWarpM) {
+        // ---------------------------------------------------------- MMAs
+        if (lane == 0) {
+            const uint32_t idS = idesc_bf16(128, kStepKeys, 0), idO = idesc_bf16(128, 256, 1);
+            SegCursor cv = cur;
+            Seg sv;
+            bool hq = cur.next(p, w, sg), hv = cv.next(p, w, sv), ok = true;
+            int tq = hq ? sg.s0 : 0, tv = hv ? sv.s0 : 0;
+            uint32_t gq = 0, gv = 0, kq = 0, kv = 0;  // steps and segments of the two cursors
+            const SDesc pd = sdesc_split(sdesc_sw128(smem_u32(sm + oP), 16, 1024));
+            uint64_t idle = 0;
+            while (ok && hv) {
+                bool issued = false;
+                if (hq && (tq != sg.s0 || mbar_test(qready, kq & 1)) && mbar_test(&kfull[gq & 1], (gq >> 1) & 1) &&
+                    (gq == 0 || mbar_test(sfree, (gq - 1) & 1))) {
+                    tc_fence_after();
+                    const uint32_t kb = smem_u32(sm) + (gq & 1) * kStage;
+                    const SDesc kd = sdesc_split(sdesc_sw128(kb, 16, 1024));
+                    const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oQ), 16, 1024));
+                    const uint32_t dS = tmem + kColS;
+#pragma unroll
+                    for (int c = 0; c < 8; c++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const uint64_t b = kd.at(c * (kKSlice / 16) + 2 * k);
+                            if (c < 4) mma_bf16_ts(dS, tmem + kColQ + 32 * c + 8 * k, b, idS, (c | k) != 0 ? 1u : 0u);
+                            else mma_bf16_ss(dS, qd.at((c - 4) * 1024 + 2 * k), b, idS, 1u);
+                        }
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const uint64_t b = kd.at(8 * (kKSlice / 16) + 2 * k);
+                        mma_bf16_ts(dS, tmem + kColR + 8 * k, b, idS, 1u);
+                        mma_bf16_ts(dS, tmem + kColR + 32 + 8 * k, b, idS, 1u);
+                    }
+                    gq++;
+                    if (++tq == sg.s1) {
+                        mma_commit(qfree);
+                        kq++;
+                        hq = cur.next(p, w, sg);
+                        if (hq) tq = sg.s0;
+                    }
+                    mma_commit(sfull);
+                    issued = true;
+                }
+                if (gv < gq && mbar_test(pready, gv & 1) && (tv != sv.s0 || kv == 0 || mbar_test(ofree, (kv - 1) & 1))) {
+                    tc_fence_after();
+                    const uint32_t vb = smem_u32(sm) + (gv & 1) * kStage + 4 * half * kKSlice;
+                    const SDesc vd = sdesc_split(sdesc_sw128(vb, kKSlice, 1024));
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma_bf16_ss(tmem + kColO, pd.at(2 * k), vd.at(128 * k), idO, tv != sv.s0 || k > 0 ? 1u : 0u);
+                    mma_commit(&kempty[gv & 1]);
+                    mma_commit(pvdone);
+                    gv++;
+                    if (++tv == sv.s1) {
+                        kv++;
+                        hv = cv.next(p, w, sv);
+                        if (hv) tv = sv.s0;
+                    }
+                    issued = true;
+                }
+                if (issued) {
+                    idle = 0;
+                } else {
+                    const uint64_t now = globaltimer();
+                    if (idle == 0) idle = now;
+                    if (*abort_flag) ok = false;
+                    else if (now - idle > wlim) {
+                        *abort_flag = 1;
+                        ok = false;
+                    }
+                }
+            }
+        }
+    } else {
+        // -------------------------------------------------------- softmax
+        const int q4 = warp & 3, hf = warp >> 2, r = q4 * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+        uint32_t g = 0, sk = 0;
+        bool ok = true;
+        for (; ok && cur.next(p, w, sg); sk++) {
+            const int ti = w.tpt > 1 || p.n_h == 128 ? r / p.n_h : 0, h = sg.hc * 128 + r - ti * p.n_h;
+            const bool live = ti < sg.n_tok && h < p.n_h && (ti == 0 || w.hchunks == 1);
+            const SeqView v{sg.tok0 - sg.i0, sg.q_len, sg.kv, false};
+            int lo = 0, hi = 0;
+            if (live) seq_range(p, v, sg.i0 + ti, &lo, &hi);
+            float m = -INFINITY, l = 0.f;
+            bool bad = false;  // a key outside the row's range is not finite
+            for (int t = sg.s0; t < sg.s1; t++, g++) {
+                ok = warp_all(mbar_wait(sfull, g & 1, abort_flag, wlim));
+                if (!ok) break;
+                tc_fence_after();
+                float s[32];
+                tmem_ld32(trow + kColS + 32 * hf, s);
+                const uint32_t km = kmask[(g & 1) * 4 + 2 * hf] | ((uint32_t)kmask[(g & 1) * 4 + 2 * hf + 1] << 16);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfree);
+                const int k0 = sg.lo + t * kStepKeys + 32 * hf;
+                const int c0 = max(lo - k0, 0), c1 = min(hi - k0, 32);
+                uint32_t rm = c1 > c0 ? (c1 >= 32 ? 0xffffffffu : (1u << c1) - 1u) & ~((1u << (c0 & 31)) - 1u) : 0u;
+                rm &= km;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (!warp_all(rm == 0xffffffffu)) {
+#pragma unroll
+                    for (int c = 0; c < 32; c++) {
+                        const bool in = (rm >> c) & 1;
+                        bad |= !in && !(fabsf(s[c]) < INFINITY);
+                        s[c] = in ? s[c] : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c++) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+                const float mh = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (t == sg.s0 && sk > 0) {  // the other warp has read the last segment's sums from here
+                    ok = warp_all(mbar_wait(&lbar[q4], 1, abort_flag, wlim));
+                    if (!ok) break;
+                }
+                xm[((g & 1) * 2 + hf) * 128 + r] = mh;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&xbar[2 * q4 + (g & 1)]);
+                ok = warp_all(mbar_wait(&xbar[2 * q4 + (g & 1)], (g >> 1) & 1, abort_flag, wlim));
+                if (!ok) break;
+                const float mt = fmaxf(mh, xm[((g & 1) * 2 + (hf ^ 1)) * 128 + r]) * p.scale_log2;
+                bool resc = false;
+                float alpha = 1.f;
+                if (mt > m + kGrow || (m == -INFINITY && mt > m)) {
+                    if (m != -INFINITY) {
+                        resc = true;
+                        alpha = ex2(m - mt);
+                    }
+                    m = mt;
+                }
+                const bool some = m != -INFINITY;
+                const float neg = some ? -m : 0.f;
+                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pw[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float e0 = ex2(fmaf(s[c], p.scale_log2, neg)), e1 = ex2(fmaf(s[c + 1], p.scale_log2, neg));
+                    ps[c & 3] += e0;
+                    ps[(c + 1) & 3] += e1;
+                    pw[c / 2] = pack_bf16x2(e0, e1);
+                }
+                l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+                if (g > 0) {  // P and O are free once the product before has completed
+                    ok = warp_all(mbar_wait(pvdone, (g - 1) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                }
+                if (__any_sync(0xffffffffu, resc)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 128 * hf; c < 128 * hf + 128; c += 32) {
+                        float o[32];
+                        tmem_ld32(trow + kColO + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++) o[i] *= alpha;
+                        tmem_st32(trow + kColO + c, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+#pragma unroll
+                for (int u = 0; u < 4; u++)
+                    *reinterpret_cast<uint4 *>(sm + oP + sw128(r, 4 * hf + u)) =
+                        make_uint4(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready);
+            }
+            if (!ok) break;
+            xm[((g & 1) * 2 + hf) * 128 + r] = bad ? NAN : l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&lbar[q4]);
+            ok = warp_all(mbar_wait(pvdone, (g - 1) & 1, abort_flag, wlim)) &&
+                 warp_all(mbar_wait(&lbar[q4], 0, abort_flag, wlim));
+            if (!ok) break;
+            tc_fence_after();
+            // (a row that sees NaN or infinity itself has NaN sums too, and comes
+            // out the same either way)
+            const float lt = (bad ? NAN : l) + xm[((g & 1) * 2 + (hf ^ 1)) * 128 + r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&lbar[q4]);
+            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const int tok = sg.tok0 + ti, col0 = 256 * half + 128 * hf;
+            const float lse2 = lt > 0.f ? m + log2f(lt) : -INFINITY;
+            uint8_t *dst = nullptr;
+            float *pdst = nullptr;
+            if (sg.slot >= 0) {
+                pdst = w.part_o + ((size_t)sg.slot * 128 + r) * kDL + col0;
+                if (half == 0 && hf == 0) w.part_lse[sg.slot * 128 + r] = lse2;
+            } else if (live) {
+                dst = (uint8_t *)((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs + col0);
+                if (half == 0 && hf == 0) p.lse[(size_t)tok * p.n_h + h] = lse2 * kLn2;
+            }
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                tmem_ld32(trow + kColO + 128 * hf + c, o);
+                tmem_wait_ld();
+                if (pdst && live) {
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        *reinterpret_cast<float4 *>(pdst + c + 4 * u) =
+                            lt > 0.f ? make_float4(o[4 * u] * inv, o[4 * u + 1] * inv, o[4 * u + 2] * inv, o[4 * u + 3] * inv)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                } else if (dst) {
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (lt > 0.f)
+                            x = make_uint4(pack_bf16x2(o[8 * u] * inv, o[8 * u + 1] * inv),
+                                           pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
+                                           pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                                           pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
+                        *reinterpret_cast<uint4 *>(dst + 2 * c + 16 * u) = x;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ofree);
+            // Rows whose product met a key that is not finite and not theirs (0 x NaN):
+            // the whole warp evaluates them one by one over the row's own keys.
+            __syncwarp();
+            uint32_t redo = __ballot_sync(0xffffffffu, live && lt != lt);
+            while (redo) {
+                const int who = __ffs(redo) - 1;
+                redo &= redo - 1;
+                const int rti = __shfl_sync(0xffffffffu, ti, who), rh = __shfl_sync(0xffffffffu, h, who);
+                const int ka = max(__shfl_sync(0xffffffffu, lo, who), sg.lo + sg.s0 * kStepKeys);
+                const int kb = min(__shfl_sync(0xffffffffu, hi, who), sg.lo + sg.s1 * kStepKeys);
+                const int rtok = sg.tok0 + rti;
+                float acc[18], rmx, rl;
+                paged_row<__nv_bfloat16, KIND, 18, 1>(
+                    p, sg.seq, (const __nv_bfloat16 *)p.q + (long long)rtok * p.q_ts + (long long)rh * p.q_hs,
+                    sg.kv - sg.q_len + sg.i0 + rti, ka, kb, acc, rmx, rl);
+                const bool rsome = rl != 0.f;
+                const float ri = rsome ? 1.f / rl : 0.f, rlse = rsome ? rmx + log2f(rl) : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int d = lane + 32 * i;
+                    if (d < col0 || d >= col0 + 128) continue;
+                    const float val = rsome ? acc[i] * ri : 0.f;
+                    if (sg.slot >= 0)
+                        w.part_o[((size_t)sg.slot * 128 + q4 * 32 + who) * kDL + d] = val;
+                    else
+                        ((__nv_bfloat16 *)p.o)[(long long)rtok * p.o_ts + (long long)rh * p.o_hs + d] =
+                            __float2bfloat16_rn(val);
+                }
+                if (lane == 0 && half == 0 && hf == 0) {
+                    if (sg.slot >= 0) w.part_lse[sg.slot * 128 + q4 * 32 + who] = rlse;
+                    else p.lse[(size_t)rtok * p.n_h + rh] = rlse * kLn2;
+                }
+            }
+        }
+    }
+
+    // ---------------------------------------------------------- teardown
+    __syncthreads();
+    if (*abort_flag && warp == kWarpM && lane == 0) {
+        volatile int never = 0;
+        mma_commit(drain);
+        mbar_wait(drain, 0, &never);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpM) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
+}
+
+// Joins the parts of the tiles that pairs shared. CTA (i, y): the tile that
+// pair i goes on with and pair i - 1 began, rows y, y + gridDim.y, ...; four
+// groups of 128 threads take every fourth part, four columns to a thread.
+__global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPlan w) {
+    __shared__ float wt[kPairs + 1];
+    __shared__ float4 sum[3][128];
+    pdl_wait();
+    const long long per = w.head->per, total = w.head->total, b = per * (blockIdx.x + 1);
+    if (b >= total) return;
+    const int r = w.first[blockIdx.x + 1];
+    // first[] names the tile at the pair's first step: one that begins there is not shared
+    const long long t0 = w.start[r], t1 = w.start[r + 1];
+    if (t0 >= b || t0 / per != blockIdx.x) return;
+    const int4 tl = w.tiles[r];
+    const SeqView v = seq_view(p, tl.x);
+    const int p0 = blockIdx.x, n = (int)((t1 - 1) / per) - p0 + 1;
+    const int grp = threadIdx.x >> 7, c = threadIdx.x & 127;
+    for (int row = blockIdx.y; row < 128; row += gridDim.y) {
+        const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.z * 128 + row - ti * p.n_h;
+        if (ti >= min(w.tpt, v.q_len - tl.y) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
+        // part k: pair p0 + k, its slot 1 for the tile's beginning, 0 after it
+        __syncthreads();
+        if (threadIdx.x < n) wt[threadIdx.x] = w.part_lse[(2 * (p0 + threadIdx.x) + (threadIdx.x == 0)) * 128 + row];
+        __syncthreads();
+        float m = -INFINITY, l = 0.f;
+        for (int k = 0; k < n; k++) m = wt[k] != wt[k] || m != m ? NAN : fmaxf(m, wt[k]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (m != -INFINITY) {
+            for (int k = 0; k < n; k++) l += exp2f(wt[k] - m);
+#pragma unroll 4
+            for (int k = grp; k < n; k += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(
+                                           w.part_o + ((size_t)(2 * (p0 + k) + (k == 0)) * 128 + row) * kDL) + c);
+                const float f = exp2f(wt[k] - m) / l;
+                acc.x = fmaf(f, x.x, acc.x);
+                acc.y = fmaf(f, x.y, acc.y);
+                acc.z = fmaf(f, x.z, acc.z);
+                acc.w = fmaf(f, x.w, acc.w);
+            }
+        }
+        if (grp) sum[grp - 1][c] = acc;
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+            for (int k = 0; k < 3; k++) {
+                acc.x += sum[k][c].x;
+                acc.y += sum[k][c].y;
+                acc.z += sum[k][c].z;
+                acc.w += sum[k][c].w;
+            }
+            const int tok = v.q0 + tl.y + ti;
+            *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs + 4 * c) =
+                make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+            if (c == 0) p.lse[(size_t)tok * p.n_h + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+        }
+    }
+}
+
+template <int KIND> cudaError_t launch_t(const Paged &p, const PagedPlan &w, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(k_paged_tc<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    return launch_pdl(k_paged_tc<KIND>, dim3(2 * kPairs), dim3(kThreads), kSmem, st, p, w);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(const Paged &p, const PagedPlan &w, cudaStream_t st) {
+    cudaError_t e = p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(p, w, st) : launch_t<DSPARK_CACHE_FP8>(p, w, st);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    return launch_pdl(k_paged_join, dim3(kPairs - 1, 16), dim3(512), 0, st, p, w);
+}
+
+}  // namespace dspark

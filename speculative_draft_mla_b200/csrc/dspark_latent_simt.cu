@@ -10,7 +10,7 @@
 // four keys) and the L1 reads of the keys, which the heads of a block share.
 #include <algorithm>
 
-#include "dspark_latent.cuh"
+#include "dspark_latent_paged.cuh"
 
 namespace dspark {
 
@@ -19,13 +19,6 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 4;  // warps per CTA
-
-template <int N> __device__ __forceinline__ void warp_sum_all(float (&x)[N]) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; i++) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
-}
 
 // Element d of the query row, rope slice turned to the row's position.
 template <typename T>
@@ -105,13 +98,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_lat_fwd_simt(Prob p, const T *_
             s[u] = t + u < nk ? s[u] * p.scale_log2 : -INFINITY;
             mn = fmaxf(mn, s[u]);
         }
-        const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
+        const float mu = mn == -INFINITY ? 0.f : mn;  // (scores of -inf or NaN only)
+        const float al = exp2f(m - mu);
         l *= al;
 #pragma unroll
         for (int i = 0; i < NL; i++) acc[i] *= al;
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-            const float e = t + u < nk ? exp2f(s[u] - mn) : 0.f;
+            const float e = t + u < nk ? exp2f(s[u] - mu) : 0.f;
             l += e;
             if (t + u < nk) {
 #pragma unroll
@@ -120,7 +114,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lat_fwd_simt(Prob p, const T *_
         }
         m = mn;
     }
-    const float inv = 1.f / l;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int i = 0; i < NL; i++)
         if (lane + 32 * i < p.d_c) o[row * p.d_c + lane + 32 * i] = from_f<T>(acc[i] * inv);
@@ -294,27 +288,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_lat_bwd_k_simt(Prob p, const T 
 
 // ---------------------------------------------------------------------------
 // Attention over the paged cache, one warp per (token, head).
-template <int KIND> struct CacheRow;
-template <> struct CacheRow<DSPARK_CACHE_F32> {
-    static __device__ __forceinline__ float at(const uint8_t *row, int d, int d_l, int d_r) {
-        return reinterpret_cast<const float *>(row)[d];
-    }
-};
-template <> struct CacheRow<DSPARK_CACHE_BF16> {
-    static __device__ __forceinline__ float at(const uint8_t *row, int d, int d_l, int d_r) {
-        return to_f(reinterpret_cast<const __nv_bfloat16 *>(row)[d]);
-    }
-};
-template <> struct CacheRow<DSPARK_CACHE_FP8> {
-    static __device__ __forceinline__ float at(const uint8_t *row, int d, int d_l, int d_r) {
-        if (d >= d_l) return to_f(reinterpret_cast<const __nv_bfloat16 *>(row + d_l)[d - d_l]);
-        const float s = reinterpret_cast<const float *>(row + d_l + 2 * d_r)[d >> 7];
-        __nv_fp8_e4m3 v;
-        v.__x = row[d];
-        return (float)v * s;
-    }
-};
-
 template <typename T, int KIND, int NL>
 __global__ void __launch_bounds__(kWarps * 32) k_paged_simt(const Paged p) {
     const int lane = threadIdx.x & 31;
@@ -323,7 +296,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_simt(const Paged p) {
     const int tok = (int)(id / p.n_h), h = (int)(id % p.n_h);
     // the sequence of the token: the warp scans the starts 32 at a time
     int s = -1;
-    SeqView sv{};
     for (int s0 = 0; s0 < p.n_seq && s < 0; s0 += 32) {
         bool mine = false;
         if (s0 + lane < p.n_seq) {
@@ -334,69 +306,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_simt(const Paged p) {
         if (any) s = s0 + __ffs(any) - 1;
     }
     if (s < 0) return;  // behind the last sequence
-    sv = seq_view(p, s);
+    const SeqView sv = seq_view(p, s);
     int lo, hi;
     seq_range(p, sv, tok - sv.q0, &lo, &hi);
-    const int dk = p.d_l + p.d_r, pos_q = sv.kv - sv.q_len + tok - sv.q0;
     const T *qrow = (const T *)p.q + (long long)tok * p.q_ts + (long long)h * p.q_hs;
-    float qv[NL], acc[NL];
-#pragma unroll
-    for (int i = 0; i < NL; i++) {
-        const int d = lane + 32 * i;
-        float val = 0.f;
-        if (d < p.d_l) {
-            val = to_f(qrow[d]);
-        } else if (d < dk) {
-            const int r = d - p.d_l;
-            const float2 t = rope_cs(pos_q, p.freq.f[r >> 1]);
-            const float x0 = to_f(qrow[p.d_l + (r & ~1)]), x1 = to_f(qrow[p.d_l + (r | 1)]);
-            val = (r & 1) ? x0 * t.y + x1 * t.x : x0 * t.x - x1 * t.y;
-        }
-        qv[i] = val;
-        acc[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int k0 = lo; k0 < hi; k0 += 4) {
-        float sc[4], kv[4][NL];
-        bool ok[4];
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const int key = k0 + u;
-            int page = -1;
-            if (key < hi) page = p.table[(size_t)s * p.max_pages + key / p.page_size];
-            ok[u] = page >= 0 && page < p.n_pages;
-            sc[u] = 0.f;
-            const uint8_t *krow =
-                (const uint8_t *)p.cache + ((size_t)(ok[u] ? page : 0) * p.page_size + key % p.page_size) * p.row_bytes;
-#pragma unroll
-            for (int i = 0; i < NL; i++) {
-                const int d = lane + 32 * i;
-                kv[u][i] = ok[u] && d < dk ? CacheRow<KIND>::at(krow, d, p.d_l, p.d_r) : 0.f;
-                sc[u] = fmaf(qv[i], kv[u][i], sc[u]);
-            }
-        }
-        warp_sum_all(sc);
-        float mn = m;
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            sc[u] = ok[u] ? sc[u] * p.scale_log2 : -INFINITY;
-            mn = fmaxf(mn, sc[u]);
-        }
-        const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        l *= al;
-#pragma unroll
-        for (int i = 0; i < NL; i++) acc[i] *= al;
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            if (!ok[u]) continue;
-            const float e = exp2f(sc[u] - mn);
-            l += e;
-#pragma unroll
-            for (int i = 0; i < NL; i++) acc[i] = fmaf(e, kv[u][i], acc[i]);
-        }
-        m = mn;
-    }
-    const bool some = m != -INFINITY;
+    float acc[NL], m, l;
+    const bool gone = paged_row<T, KIND, NL, 4>(p, s, qrow, sv.kv - sv.q_len + tok - sv.q0, lo, hi, acc, m, l);
+    if (gone && lane == 0) atomicOr(p.err, kErrPage);
+    const bool some = l != 0.f;  // (NaN counts)
     T *orow = (T *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs;
 #pragma unroll
     for (int i = 0; i < NL; i++)

@@ -352,15 +352,19 @@ def test_paged_later_tokens_do_not_matter(kind):
     q = torch.randn(9, n_h, 576, generator=torch.Generator().manual_seed(53))
     q = q.to(torch.float32 if kind == "f32" else torch.bfloat16).cuda()
     args = (table.cuda(), qs.cuda(), kv.cuda(), 150)
-    o, lse, _ = capi.latent_attn_paged(q, cache, *args)
+    val, err = reference(q.double().cpu().numpy(), lat, rope, table.numpy(), qs.numpy(), kv.numpy(), page,
+                         capi.LATENT_SCALE, True, 0, kind != "f32")
     rows = cache.view(n_pages * page, -1)
     for s, p in ((0, 147), (1, 38)):
         rows[int(table[s, p // page]) * page + p % page] = 0xff if kind == "fp8" else float("nan")
-    o2, lse2, _ = capi.latent_attn_paged(q, cache, *args)
-    for a, b in ((0, 3), (6, 7)):  # positions 144 .. 146 of the first, 37 of the second
-        assert torch.equal(o[a:b], o2[a:b]) and torch.equal(lse[a:b], lse2[a:b])
+    o, lse, _ = capi.latent_attn_paged(q, cache, *args)
+    # positions 144 .. 146 of the first, 37 of the second: the values they have without the bad rows. (Not the same
+    # bits: such rows are summed in another order, both within the bounds of the exact result.)
+    for a, b in ((0, 3), (6, 7)):
+        lp.check("o", o[a:b], val["o"][a:b], err["o"][a:b])
+        lp.check("lse", lse[a:b], val["lse"][a:b], err["lse"][a:b])
     for a, b in ((3, 6), (7, 9)):
-        assert torch.isnan(o2[a:b].float()).all()
+        assert torch.isnan(o[a:b].float()).all()
 
 
 def test_paged_bad_pages_and_lengths():

@@ -20,6 +20,7 @@ struct LatWsLayout {
     size_t fwd_total;
     size_t dvec;   // float [B, n_h, 5N]: D = sum_k P dP (CUDA-core backward)
     size_t dacc;   // float [B, L, d_l + d_r]: key gradients (tensor-core backward)
+    size_t q_rot;  // bf16 [B, n_h, 5N, d_r]: turned rope queries (tensor-core backward)
     size_t total;
 };
 
@@ -40,6 +41,7 @@ inline LatWsLayout lat_layout(const Prob &p) {
     const bool tc = lat_bwd_tc_supported(p);
     w.dvec = off;      off = align256(off + (tc ? 0 : sizeof(float) * (size_t)p.B * p.n_h * p.R));
     w.dacc = off;      off = align256(off + (tc ? sizeof(float) * (size_t)p.B * p.L * p.dqk : 0));
+    w.q_rot = off;     off = align256(off + (tc ? 2 * (size_t)p.B * p.n_h * p.R * p.d_r : 0));
     w.total = off;
     return w;
 }
@@ -47,7 +49,7 @@ inline LatWsLayout lat_layout(const Prob &p) {
 struct LatWs {
     Ws base;  // err, cnt, sorted_n, sorted_a, rope
     float *kr_f32;
-    __nv_bfloat16 *kr_hi, *kr_lo;
+    __nv_bfloat16 *kr_hi, *kr_lo, *q_rot;
     float *dvec, *dacc;
 };
 
@@ -65,6 +67,7 @@ inline LatWs lat_view(const Prob &p, void *ws) {
     w.kr_lo = w.kr_hi + (size_t)p.B * p.L * p.d_r;
     w.dvec = (float *)(c + l.dvec);
     w.dacc = (float *)(c + l.dacc);
+    w.q_rot = (__nv_bfloat16 *)(c + l.q_rot);
     return w;
 }
 
@@ -76,6 +79,8 @@ cudaError_t launch_lat_fwd_tc(const Prob &p, const void *q, const void *c, void 
                               cudaStream_t st);
 cudaError_t launch_lat_fwd_simt(const Prob &p, const void *q, const void *c, const int32_t *anchors,
                                 const uint8_t *keep, void *o, float *lse, const LatWs &ws, cudaStream_t st);
+cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const int32_t *anchors, const float *lse,
+                              const void *dout, void *dq, void *dc, void *dkr, const LatWs &ws, cudaStream_t st);
 cudaError_t launch_lat_bwd_simt(const Prob &p, const void *q, const void *c, const int32_t *anchors,
                                 const uint8_t *keep, const float *lse, const void *dout, void *dq, void *dc,
                                 void *dkr, const LatWs &ws, cudaStream_t st);

@@ -1,0 +1,673 @@
+// Tensor-core (tcgen05 / TMEM / TMA) backward of the latent draft attention:
+// bf16, 512-wide latents, 64-wide rope keys, windows of at most 128.
+//
+// Tile: up to 22 heads x 5 rows of one kept block, whose rows all see the same
+// keys (up to 127 context and 5 draft). Recomputed: S = Q K^T and dP = dO C^T
+// over all of them, P = exp(S - LSE), D = sum_k P dP (the row is whole, so the
+// forward's O is not needed), dS = scale P (dP - D). Then per 64 columns c:
+//   dq_c = dS K_c                       rows x columns
+//   dk_c = dS^T Q_c + P^T dO_c          context keys x columns
+//   dd_c = Q_c^T dS_d, dO_c^T P_d       columns x draft keys (one product: the two
+//                                       column sets are its 128 rows, the two key
+//                                       sets its 32 columns)
+// P and dS go through shared memory, where rows-by-keys tiles serve as they are
+// (dS K) and transposed (dS^T Q). Key gradients of all heads and of the blocks
+// whose windows overlap meet in an fp32 accumulator [B, L, 576] by vector
+// reductions; the last launch turns its rope part back and rounds.
+//
+// The 132 x 576 fp32 key gradients of a block (304 KB) fit neither tensor
+// memory nor shared memory beside the keys, so a tile's share leaves the SM as
+// it is formed, and keys, Q and dO come in 64-column slices through two rings,
+// twice per tile: for S and dP, and, from L2, for the gradients. The products of
+// the gradients of a tile are interleaved with S and dP of the next, slice by
+// slice, sharing the slice of the keys within a block. What bounds it is this
+// traffic between SMs and L2 (reads 1.1 MB, writes 0.43 MB a tile against 0.36 MB
+// that DRAM has to move).
+//
+// Sums of key gradients are fp32 in whatever order the tiles finish: two runs
+// may differ in the last bits before the rounding to bf16. P and dS are bf16
+// operands, the rope slices of Q and K one bf16 each (the gradients are bf16;
+// the forward's LSE is formed more exactly).
+//
+// TMEM: S 0..143, dP 144..287, three product buffers 288..479, dd 480..511.
+// Warps 0-7 softmax (warps w and w + 4 share 32 rows, 64 context keys each);
+// 0-3 then store dq, 4-7 reduce dk and dd; 8 loads keys, 9 Q and dO, 10 issues
+// the MMAs. Every wait is bounded.
+#include <algorithm>
+
+#include "dspark_latent_tc.cuh"
+
+namespace dspark {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kDL = 512, kDR = 64, kDK = kDL + kDR;
+constexpr int kSlices = 9;
+constexpr int kKeys = 144, kKSlot = kKeys * 128, kKSlots = 4;
+constexpr int kHeads = 22, kRows = 112;            // rows of a tile, padded to the K steps of 16
+constexpr int kSlot = kRows * 128, kPair = 2 * kSlot, kPairs2 = 3;  // Q slice, dO slice
+constexpr int oK = 0, oPair = kKSlots * kKSlot;
+constexpr int oDS = oPair + kPairs2 * kPair;       // dS, context keys: two slices of 64 keys
+constexpr int oPr = oDS + 2 * kSlot;               // P
+constexpr int oDD = oPr + 2 * kSlot;               // draft keys: [2 x 64 rows][16 dS, 16 P][128 B]
+constexpr int oX = oDD + 2 * 32 * 128;             // D halves [2][128]
+constexpr int oBar = oX + 1024;
+constexpr int kSmem = oBar + 512 + 1024;
+static_assert(kHeads * kBlock <= kRows && kSmem <= 232448, "shared memory");
+static_assert(kSlot % 1024 == 0 && oDD % 1024 == 0, "swizzle atoms");
+constexpr uint32_t kColS = 0, kColP = kKeys, kColC = 2 * kKeys, kColD = kColC + 3 * 64;
+constexpr int kWarpK = 8, kWarpQ = 9, kWarpM = 10, kThreads = 11 * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Args {
+    int n_h, S, N, W, R, B, L;
+    int ctxpad, hp, nsplit, tiles, per, n_work;
+    float scale, scale_log2;
+    const int32_t *cnt, *sorted_n, *sorted_a;
+    const float2 *tab;
+    const float *lse;
+    __nv_bfloat16 *dq;
+    float *dacc;
+    uint32_t *err;
+    uint64_t wait_ns;
+    bool wide;
+};
+
+__device__ __forceinline__ void red2(float *a, float x, float y) {
+    asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void red1(float *a, float x) {
+    asm volatile("red.global.add.f32 [%0], %1;" ::"l"(a), "f"(x) : "memory");
+}
+// 16 lanes (from the address's lane) x 64 columns: register 4 g + 2 i + e of
+// lane t is row t / 4 + 8 i, column 8 g + 2 (t % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+
+// The CTA's tiles in order, over its items.
+struct Tile {
+    int b, n, a, h0, nh;
+    bool fresh;  // first of its item: other keys than the tile before
+};
+struct TileCursor {
+    DraftCursor cur;
+    DraftItem it;
+    int w, t, G;
+    bool open;
+    __device__ __forceinline__ TileCursor(const Args &p)
+        : cur{p.cnt, p.sorted_n, p.sorted_a, p.B, p.N, p.nsplit, p.tiles, p.per}, w(blockIdx.x), t(0),
+          G(gridDim.x), open(false) {}
+    __device__ __forceinline__ bool next(const Args &p, Tile &o) {
+        o.fresh = !open;
+        if (!open) {
+            if (w >= p.n_work || !cur.at(w, it)) return false;
+            t = it.t0;
+            open = true;
+        }
+        o.b = it.b;
+        o.n = it.n;
+        o.a = it.a;
+        o.h0 = t * p.hp;
+        o.nh = min(p.hp, p.n_h - o.h0);
+        if (++t == it.t1) {
+            open = false;
+            w += G;
+        }
+        return true;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_lat_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
+                 const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_c,
+                 const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_c5,
+                 const __grid_constant__ CUtensorMap tm_h5, const Args p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + kKSlots;
+    uint64_t *qfull = kempty + kKSlots, *qempty = qfull + kPairs2;
+    uint64_t *sfull = qempty + kPairs2, *pds = sfull + 1, *drain = sfull + 2;
+    uint64_t *cfull = sfull + 3, *cfree = cfull + 6, *dfull = cfree + 3, *dfree = dfull + 1, *lbar = dfull + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lbar + 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(lbar + 5);
+    float *xd = reinterpret_cast<float *>(sm + oX);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t wlim = p.wait_ns;
+
+    // slots of keys and rows that no copy ever writes, and P, dS, stay or start zero
+    for (int e = threadIdx.x; e < oX / 16; e += kThreads) reinterpret_cast<uint4 *>(sm)[e] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * kKSlots; i++) mbar_init(&kfull[i], 1);
+        for (int i = 0; i < 2 * kPairs2; i++) mbar_init(&qfull[i], 1);
+        mbar_init(sfull, 1);
+        mbar_init(pds, 8);
+        mbar_init(drain, 1);
+        for (int i = 0; i < 6; i++) mbar_init(&cfull[i], 1);  // [dq, dk][buffer]
+        for (int i = 0; i < 3; i++) mbar_init(&cfree[i], 4);
+        mbar_init(dfull, 1);
+        mbar_init(dfree, 4);
+        for (int i = 0; i < 4; i++) mbar_init(&lbar[i], 2);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpM) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    pdl_wait();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    uint32_t n_issued = 0;  // the loaders' copies
+
+    // Step k: gradients of tile k - 1 and scores of tile k, slice by slice; the
+    // loaders and the issuer walk the same steps.
+    if (warp == kWarpK) {
+        // -------------------------------------------------------- keys
+        if (lane == 0) {
+            TileCursor cu(p);
+            Tile cur, prev;
+            const uint32_t bytes = (p.W - 1 + kBlock) * 128;
+            bool ok = true, hp = false;
+            auto load = [&](const Tile &t, int c) {
+                const uint32_t s = n_issued % kKSlots;
+                if (n_issued >= kKSlots && !mbar_wait(&kempty[s], (n_issued / kKSlots - 1) & 1, abort_flag, wlim))
+                    return false;
+                uint8_t *dst = sm + oK + s * kKSlot;
+                const int x = c < 8 ? 64 * c : 0;
+                mbar_arrive_expect_tx(&kfull[s], bytes);
+                if (p.W > 1) tma_load_3d(dst, c < 8 ? &tm_c : &tm_h, &kfull[s], x, t.a - (p.W - 1), t.b);
+                tma_load_3d(dst + p.ctxpad * 128, c < 8 ? &tm_c5 : &tm_h5, &kfull[s], x, p.S + kBlock * t.n, t.b);
+                n_issued++;
+                return true;
+            };
+            for (;;) {
+                const bool has = cu.next(p, cur);
+                for (int c = 0; ok && c < kSlices; c++) {
+                    if (hp) ok = load(prev, c);
+                    if (ok && has && (!hp || cur.fresh)) ok = load(cur, c);
+                }
+                if (!ok || !has) break;
+                prev = cur;
+                hp = true;
+            }
+        }
+    } else if (warp == kWarpQ) {
+        // ---------------------------------------------------- Q and dO
+        if (lane == 0) {
+            TileCursor cu(p);
+            Tile cur, prev;
+            bool ok = true, hp = false;
+            const uint32_t bytes = p.hp * kBlock * 128;
+            auto load = [&](const Tile &t, int c) {
+                const uint32_t s = n_issued % kPairs2;
+                if (n_issued >= kPairs2 && !mbar_wait(&qempty[s], (n_issued / kPairs2 - 1) & 1, abort_flag, wlim))
+                    return false;
+                uint8_t *dst = sm + oPair + s * kPair;
+                mbar_arrive_expect_tx(&qfull[s], c < 8 ? 2 * bytes : bytes);
+                if (c < 8) {
+                    tma_load_4d(dst, &tm_q, &qfull[s], 64 * c, kBlock * t.n, t.h0, t.b);
+                    tma_load_4d(dst + kSlot, &tm_g, &qfull[s], 64 * c, kBlock * t.n, t.h0, t.b);
+                } else {
+                    tma_load_4d(dst, &tm_qr, &qfull[s], 0, kBlock * t.n, t.h0, t.b);
+                }
+                n_issued++;
+                return true;
+            };
+            for (;;) {
+                const bool has = cu.next(p, cur);
+                for (int c = 0; ok && c < kSlices; c++) {
+                    if (hp) ok = load(prev, c);
+                    if (ok && has) ok = load(cur, c);
+                }
+                if (!ok || !has) break;
+                prev = cur;
+                hp = true;
+            }
+        }
+    } else if (warp == kWarpM) {
+        // -------------------------------------------------------- MMAs
+        if (lane == 0) {
+            const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0), idQ = idesc_bf16(128, 64, 1);
+            const uint32_t idK = idesc_bf16_ab(128, 64, 1, 1), idD = idesc_bf16_ab(128, 32, 1, 0);
+            const int ksc = p.ctxpad / 16, ksr = (p.hp * kBlock + 15) / 16;
+            const SDesc dsr = sdesc_split(sdesc_sw128(smem_u32(sm + oDS), 16, 1024));         // rows x keys
+            const SDesc dst = sdesc_split(sdesc_sw128(smem_u32(sm + oDS), kSlot, 1024));      // keys x rows
+            const SDesc pt = sdesc_split(sdesc_sw128(smem_u32(sm + oPr), kSlot, 1024));
+            const SDesc dda = sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 32 * 128, 1024));   // rows x draft keys
+            const SDesc ddb = sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 16, 1024));         // draft keys x rows
+            TileCursor cu(p);
+            Tile cur, prev;
+            bool ok = true, hp = false;
+            uint32_t kn = 0, qn = 0, i = 0, k = 0;  // slots taken; slices of gradients; steps
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
+            for (; ok; k++) {
+                const bool has = cu.next(p, cur);
+                if (!has && !hp) break;
+                if (hp) {  // P and dS of tile k - 1 are written, its S and dP read
+                    if (!wait(pds, (k - 1) & 1)) break;
+                    tc_fence_after();
+                }
+                for (int c = 0; ok && c < kSlices; c++) {
+                    uint32_t ks = 0;
+                    if (hp) {
+                        ks = kn++ % kKSlots;
+                        const uint32_t qs = qn % kPairs2;
+                        if (!wait(&kfull[ks], ((kn - 1) / kKSlots) & 1) || !wait(&qfull[qs], (qn / kPairs2) & 1)) break;
+                        const SDesc kv = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), kKSlot, 1024));
+                        const SDesc qb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), kSlot, 1024));
+                        const SDesc gb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), kSlot, 1024));
+                        {
+                            const uint32_t n = 2 * i, buf = n % 3, u = n / 3;
+                            if (u > 0 && !wait(&cfree[buf], (u - 1) & 1)) break;
+                            tc_fence_after();
+                            const uint32_t d = tmem + kColC + 64 * buf;
+                            for (int s = 0; s < ksc; s++)
+                                mma_bf16_ss(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
+                            mma_bf16_ss(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
+                            mma_commit(&cfull[buf]);
+                        }
+                        {
+                            const uint32_t n = 2 * i + 1, buf = n % 3, u = n / 3;
+                            if (u > 0 && !wait(&cfree[buf], (u - 1) & 1)) break;
+                            tc_fence_after();
+                            const uint32_t d = tmem + kColC + 64 * buf;
+                            for (int s = 0; s < ksr; s++) {
+                                mma_bf16_ss(d, dst.at(128 * s), qb.at(128 * s), idK, s > 0);
+                                if (c < 8) mma_bf16_ss(d, pt.at(128 * s), gb.at(128 * s), idK, 1u);
+                            }
+                            mma_commit(&cfull[3 + buf]);
+                        }
+                        if (i > 0 && !wait(dfree, (i - 1) & 1)) break;
+                        tc_fence_after();
+                        for (int s = 0; s < ksr; s++)
+                            mma_bf16_ss(tmem + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
+                        mma_commit(&qempty[qs]);
+                        if (!has || cur.fresh) mma_commit(&kempty[ks]);
+                        mma_commit(dfull);  // last: nothing is in flight once its reader has it
+                        qn++;
+                        i++;
+                    }
+                    if (has) {
+                        if (!hp || cur.fresh) {
+                            ks = kn++ % kKSlots;
+                            if (!wait(&kfull[ks], ((kn - 1) / kKSlots) & 1)) break;
+                        }
+                        const uint32_t qs = qn % kPairs2;
+                        if (!wait(&qfull[qs], (qn / kPairs2) & 1)) break;
+                        tc_fence_after();
+                        const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
+                        const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), 16, 1024));
+                        const SDesc gd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), 16, 1024));
+#pragma unroll
+                        for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
+                        if (c < 8) {
+#pragma unroll
+                            for (int s = 0; s < 4; s++)
+                                mma_bf16_ss(tmem + kColP, gd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
+                        }
+                        mma_commit(&qempty[qs]);
+                        qn++;
+                        mma_commit(&kempty[ks]);
+                    }
+                }
+                if (!ok || !has) break;
+                mma_commit(sfull);
+                prev = cur;
+                hp = true;
+            }
+        }
+    } else if (warp < 8) {
+        // ------------------------------- softmax, then the products' readers
+        const int q4 = warp & 3, hf = warp >> 2, r = q4 * 32 + lane, j = r % kBlock, hl = r / kBlock;
+        const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+        TileCursor cu(p);
+        Tile cur, prev;
+        bool ok = true, hp = false;
+        uint32_t i = 0, k = 0;
+        for (; ok; k++) {
+            const bool has = cu.next(p, cur);
+            if (hp && hf == 0) {
+                // dq of tile k - 1: the rope slice turned back
+                const bool live = hl < prev.nh;
+                const size_t row = ((size_t)prev.b * p.n_h + prev.h0 + (live ? hl : 0)) * p.R + (size_t)kBlock * prev.n + j;
+                uint8_t *dst = reinterpret_cast<uint8_t *>(p.dq + row * kDK);
+                const float4 *tab = reinterpret_cast<const float4 *>(p.tab + (size_t)(prev.a + j) * (kDR / 2));
+#pragma unroll 1
+                for (int c = 0; c < kSlices; c++, i++) {
+                    const uint32_t buf = 2 * i % 3;
+                    ok = warp_all(mbar_wait(&cfull[buf], (i / 3) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float v[2][32];
+                    tmem_ld32(trow + kColC + 64 * buf, v[0]);
+                    tmem_ld32(trow + kColC + 64 * buf + 32, v[1]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cfree[buf]);
+                    if (c == 8) {
+#pragma unroll
+                        for (int u = 0; u < 16; u++) {
+                            const float4 cs = __ldg(tab + u);
+                            float *x = &v[u >> 3][4 * (u & 7)];
+                            const float x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
+                            x[0] = x0 * cs.x + x1 * cs.y;
+                            x[1] = x1 * cs.x - x0 * cs.y;
+                            x[2] = x2 * cs.z + x3 * cs.w;
+                            x[3] = x3 * cs.z - x2 * cs.w;
+                        }
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                x[e] = pack_bf16x2(v[u >> 1][16 * (u & 1) + 2 * e], v[u >> 1][16 * (u & 1) + 2 * e + 1]);
+                            st_global_32B(dst + 128 * c + 32 * u, x, p.wide);
+                        }
+                    }
+                }
+            } else if (hp) {
+                // dk: key slots 32 q4 + 16 s + lane / 4 (+ 8), eight columns to a quad
+                const int first = prev.a - (p.W - 1);
+                float *base = p.dacc + (size_t)prev.b * p.L * kDK;
+#pragma unroll 1
+                for (int c = 0; c < kSlices; c++, i++) {
+                    const uint32_t buf = (2 * i + 1) % 3;
+                    ok = warp_all(mbar_wait(&cfull[3 + buf], (i / 3) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float v[2][32];
+                    tmem_ld_16x64(trow + kColC + 64 * buf, v[0]);
+                    tmem_ld_16x64(trow + (16u << 16) + kColC + 64 * buf, v[1]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cfree[buf]);
+#pragma unroll
+                    for (int s = 0; s < 4; s++) {
+                        const int slot = 32 * q4 + 8 * s + (lane >> 2), pos = first + slot;
+                        if (slot < p.W - 1 && pos >= 0) {
+                            float *dst = base + (size_t)pos * kDK + 64 * c + 2 * (lane & 3);
+#pragma unroll
+                            for (int g = 0; g < 8; g++)
+                                red2(dst + 8 * g, v[s >> 1][4 * g + 2 * (s & 1)], v[s >> 1][4 * g + 2 * (s & 1) + 1]);
+                        }
+                    }
+                    // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20)
+                    ok = warp_all(mbar_wait(dfull, i & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float d[8];
+                    tmem_ld8(trow + kColD + (q4 >= 2 ? 16 : 0), d);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dfree);
+                    if (q4 < 2 || c < 8) {
+                        float *dst = base + (size_t)(p.S + kBlock * prev.n) * kDK + 64 * c + (r & 63);
+#pragma unroll
+                        for (int e = 0; e < kBlock; e++) red1(dst + (size_t)e * kDK, d[e]);
+                    }
+                }
+            }
+            if (!ok || !has) break;
+            // softmax of tile k: this warp's 64 context keys, warps 0 - 3 the draft keys too
+            const bool live = hl < cur.nh;
+            const float z = live ? p.lse[((size_t)cur.b * p.n_h + cur.h0 + hl) * p.R + (size_t)kBlock * cur.n + j] * kLog2e
+                                 : 0.f;
+            ok = warp_all(mbar_wait(sfull, k & 1, abort_flag, wlim));
+            if (!ok) break;
+            tc_fence_after();
+            const int lo = max(0, p.W - 1 - cur.a) - 64 * hf, hi = (live ? p.W - 1 : -1) - 64 * hf;
+            float P[64], D = 0.f, pd[8], gd[8];
+#pragma unroll
+            for (int x = 0; x < 64; x++) P[x] = 0.f;
+            const bool some = 64 * hf < p.ctxpad;  // (ctxpad is a multiple of 32: half a slice may be unused)
+            if (some) {
+#pragma unroll
+                for (int cc = 0; cc < 2; cc++) {
+                    if (64 * hf + 32 * cc >= p.ctxpad) continue;
+                    float s[32], g[32];
+                    tmem_ld32(trow + kColS + 64 * hf + 32 * cc, s);
+                    tmem_ld32(trow + kColP + 64 * hf + 32 * cc, g);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 32; x++) {
+                        const bool in = 32 * cc + x >= lo && 32 * cc + x < hi;
+                        const float e = in ? ex2(fmaf(s[x], p.scale_log2, -z)) : 0.f;
+                        P[32 * cc + x] = e;
+                        D = in ? fmaf(e, g[x], D) : D;
+                    }
+                }
+            }
+            if (hf == 0) {
+                tmem_ld8(trow + kColS + p.ctxpad, pd);
+                tmem_ld8(trow + kColP + p.ctxpad, gd);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < kBlock; x++) {
+                    pd[x] = live ? ex2(fmaf(pd[x], p.scale_log2, -z)) : 0.f;
+                    D = live ? fmaf(pd[x], gd[x], D) : 0.f;
+                }
+            }
+            xd[hf * 128 + r] = D;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&lbar[q4]);
+            ok = warp_all(mbar_wait(&lbar[q4], k & 1, abort_flag, wlim));
+            if (!ok) break;
+            D += xd[(hf ^ 1) * 128 + r];
+            if (some) {
+#pragma unroll
+                for (int cc = 0; cc < 2; cc++) {
+                    if (64 * hf + 32 * cc >= p.ctxpad) continue;
+                    float g[32];
+                    tmem_ld32(trow + kColP + 64 * hf + 32 * cc, g);
+                    tmem_wait_ld();
+                    if (r < kRows) {
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            uint32_t a[4], b[4];
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const int x = 8 * u + 2 * e;
+                                const float p0 = P[32 * cc + x], p1 = P[32 * cc + x + 1];
+                                a[e] = pack_bf16x2(p0, p1);
+                                const bool i0 = 32 * cc + x >= lo && 32 * cc + x < hi;
+                                const bool i1 = 32 * cc + x + 1 >= lo && 32 * cc + x + 1 < hi;
+                                b[e] = pack_bf16x2(i0 ? p0 * (g[x] - D) * p.scale : 0.f,
+                                                   i1 ? p1 * (g[x + 1] - D) * p.scale : 0.f);
+                            }
+                            const uint32_t at = hf * kSlot + sw128(r, 4 * cc + u);
+                            *reinterpret_cast<uint4 *>(sm + oPr + at) = make_uint4(a[0], a[1], a[2], a[3]);
+                            *reinterpret_cast<uint4 *>(sm + oDS + at) = make_uint4(b[0], b[1], b[2], b[3]);
+                        }
+                    }
+                }
+            }
+            if (hf == 0) {
+                // draft keys: one bf16 to each of their rows
+                uint8_t *dd = sm + oDD + (r >> 6) * (32 * 128) + (r & 7) * 2;
+                const int u = (r & 63) >> 3;
+#pragma unroll
+                for (int x = 0; x < kBlock; x++) {
+                    *reinterpret_cast<__nv_bfloat16 *>(dd + sw128(x, u)) =
+                        __float2bfloat16_rn(live ? pd[x] * (gd[x] - D) * p.scale : 0.f);
+                    *reinterpret_cast<__nv_bfloat16 *>(dd + sw128(16 + x, u)) = __float2bfloat16_rn(pd[x]);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pds);
+            prev = cur;
+            hp = true;
+        }
+    }
+
+    // ---------------------------------------------------------- teardown
+    __syncthreads();
+    if (*abort_flag && lane == 0) {
+        volatile int never = 0;
+        const uint32_t ring = warp == kWarpK ? kKSlots : kPairs2;
+        if (warp == kWarpK || warp == kWarpQ)
+            for (uint32_t g = n_issued > ring ? n_issued - ring : 0; g < n_issued; g++)
+                mbar_wait(warp == kWarpK ? &kfull[g % ring] : &qfull[g % ring], (g / ring) & 1, &never);
+        if (warp == kWarpM) {
+            mma_commit(drain);
+            mbar_wait(drain, 0, &never);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpM) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
+}
+
+// The queries' rope slices turned to their positions (one bf16 each), and the
+// key gradients' accumulators cleared.
+__global__ void __launch_bounds__(256) k_lat_bwd_prep(const __nv_bfloat16 *__restrict__ q,
+                                                      const int32_t *__restrict__ anchors,
+                                                      const float2 *__restrict__ tab, __nv_bfloat16 *__restrict__ out,
+                                                      float4 *__restrict__ dacc, size_t rows, size_t acc4, int n_h, int N,
+                                                      int P) {
+    pdl_wait();
+    pdl_trigger();
+    const size_t t0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, nt = (size_t)gridDim.x * blockDim.x;
+    for (size_t e = t0; e < acc4; e += nt) dacc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int R = kBlock * N;
+    // eight threads to a row, four pairs each
+    for (size_t e = t0; e < rows * 8; e += nt) {
+        const size_t row = e >> 3;
+        const int u = (int)(e & 7), r = (int)(row % (unsigned)R), b = (int)(row / (unsigned)R / (unsigned)n_h);
+        const int pos = min(max(anchors[(size_t)b * N + r / kBlock] + r % kBlock, 0), P - 1);
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + row * kDK + kDL) + u);
+        const float4 *cs = reinterpret_cast<const float4 *>(tab + (size_t)pos * (kDR / 2)) + 2 * u;
+        const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
+        auto turn = [](uint32_t w, float c, float s) {
+            const float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xffff0000u);
+            return pack_bf16x2(a * c - b * s, a * s + b * c);
+        };
+        reinterpret_cast<uint4 *>(out + row * kDR)[u] =
+            make_uint4(turn(v.x, c0.x, c0.y), turn(v.y, c0.z, c0.w), turn(v.z, c1.x, c1.y), turn(v.w, c1.z, c1.w));
+    }
+}
+
+// Accumulators to outputs: dc rounded, the rope part turned back to its
+// position and rounded. One warp per position.
+__global__ void __launch_bounds__(256) k_lat_bwd_out(const float *__restrict__ dacc, const int32_t *__restrict__ anchors,
+                                                     const float2 *__restrict__ tab, __nv_bfloat16 *__restrict__ dc,
+                                                     __nv_bfloat16 *__restrict__ dkr, int B, int S, int N, int L, int P) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (size_t)B * L) return;
+    const float4 *src = reinterpret_cast<const float4 *>(dacc + row * kDK);
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = src[lane * 2 + (i & 1) + (i >> 1) * 64];
+    const float2 x = reinterpret_cast<const float2 *>(dacc + row * kDK + kDL)[lane];
+    const int key = (int)(row % (unsigned)L), b = (int)(row / (unsigned)L);
+    int pos = key;
+    if (key >= S) pos = anchors[(size_t)b * N + (key - S) / kBlock] + (key - S) % kBlock;
+    const float2 cs = tab[(size_t)min(max(pos, 0), P - 1) * (kDR / 2) + lane];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        reinterpret_cast<uint4 *>(dc + row * kDL)[lane + 32 * i] =
+            make_uint4(pack_bf16x2(v[2 * i].x, v[2 * i].y), pack_bf16x2(v[2 * i].z, v[2 * i].w),
+                       pack_bf16x2(v[2 * i + 1].x, v[2 * i + 1].y), pack_bf16x2(v[2 * i + 1].z, v[2 * i + 1].w));
+    reinterpret_cast<uint32_t *>(dkr + row * kDR)[lane] = pack_bf16x2(x.x * cs.x + x.y * cs.y, x.y * cs.x - x.x * cs.y);
+}
+
+}  // namespace
+
+bool lat_bwd_tc_supported(const Prob &p) { return lat_tc_supported(p); }
+
+cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const int32_t *anchors, const float *lse,
+                              const void *dout, void *dq, void *dc, void *dkr, const LatWs &ws, cudaStream_t st) {
+    // (padding blocks' rows of dq are written by the preparation before this)
+    if (p.B == 0) return cudaSuccess;
+    int dev = 0, nsm = 0;
+    cudaError_t e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const size_t rows = (size_t)p.B * p.n_h * p.R, acc4 = (size_t)p.B * p.L * kDK / 4;
+    const size_t work = std::max(rows * 8, acc4);
+    count_launch();
+    e = launch_pdl(k_lat_bwd_prep, dim3((unsigned)std::min<size_t>((work + 255) / 256, (size_t)nsm * 8)), dim3(256), 0, st,
+                   (const __nv_bfloat16 *)q, anchors, (const float2 *)ws.base.rope, ws.q_rot, (float4 *)ws.dacc, rows,
+                   acc4, p.n_h, std::max(p.N, 1), p.P);
+    if (e != cudaSuccess) return e;
+    if (p.N > 0) {
+        Args a{};
+        a.n_h = p.n_h; a.S = p.S; a.N = p.N; a.W = p.W; a.R = p.R; a.B = p.B; a.L = p.L;
+        a.ctxpad = (p.W - 1 + 31) / 32 * 32;
+        a.tiles = (p.n_h + kHeads - 1) / kHeads;
+        a.hp = (p.n_h + a.tiles - 1) / a.tiles;
+        const long long blocks = (long long)p.B * p.N;
+        a.nsplit = (int)std::max<long long>(1, std::min<long long>(a.tiles, nsm / blocks));
+        a.per = (a.tiles + a.nsplit - 1) / a.nsplit;
+        a.nsplit = (a.tiles + a.per - 1) / a.per;
+        if (blocks * a.nsplit >= (1ll << 31) - 4096) return cudaErrorInvalidValue;
+        a.n_work = (int)(blocks * a.nsplit);
+        a.scale = p.scale;
+        a.scale_log2 = p.scale_log2;
+        a.cnt = ws.base.cnt;
+        a.sorted_n = ws.base.sorted_n;
+        a.sorted_a = ws.base.sorted_a;
+        a.tab = ws.base.rope;
+        a.lse = lse;
+        a.dq = (__nv_bfloat16 *)dq;
+        a.dacc = ws.dacc;
+        a.err = ws.base.err;
+        a.wait_ns = p.wait_ns;
+        a.wide = ((uintptr_t)dq & 31) == 0;
+        CUtensorMap mq, mg, mr, mc, mh, mc5, mh5;
+        const uint64_t L = p.L, B = p.B, R = p.R, H = p.n_h;
+        const uint64_t qd[4] = {kDK, R, H, B}, qs[3] = {kDK * 2, R * kDK * 2, H * R * kDK * 2};
+        const uint64_t gd[4] = {kDL, R, H, B}, gs[3] = {kDL * 2, R * kDL * 2, H * R * kDL * 2};
+        const uint64_t sd[4] = {kDR, R, H, B}, ss[3] = {kDR * 2, R * kDR * 2, H * R * kDR * 2};
+        const uint32_t qb[4] = {64, kBlock, (uint32_t)a.hp, 1};
+        const uint64_t cd[3] = {kDL, L, B}, cs[2] = {kDL * 2, L * kDL * 2};
+        const uint64_t rd[3] = {kDR, L, B}, rs[2] = {kDR * 2, L * kDR * 2};
+        const uint32_t wb[3] = {64, (uint32_t)std::max(p.W - 1, 1), 1}, db[3] = {64, kBlock, 1};
+        if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mg, dout, 4, gd, gs, qb) ||
+            !make_map_nd(&mr, ws.q_rot, 4, sd, ss, qb) || !make_map_nd(&mc, c, 3, cd, cs, wb) ||
+            !make_map_nd(&mh, ws.kr_hi, 3, rd, rs, wb) || !make_map_nd(&mc5, c, 3, cd, cs, db) ||
+            !make_map_nd(&mh5, ws.kr_hi, 3, rd, rs, db))
+            return cudaErrorInvalidValue;
+        e = cudaFuncSetAttribute(k_lat_bwd_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        count_launch();
+        e = launch_pdl(k_lat_bwd_tc, dim3(std::min(a.n_work, nsm)), dim3(kThreads), kSmem, st, mq, mg, mr, mc, mh, mc5,
+                       mh5, a);
+        if (e != cudaSuccess) return e;
+    }
+    count_launch();
+    return launch_pdl(k_lat_bwd_out, dim3((unsigned)(((size_t)p.B * p.L + 7) / 8)), dim3(256), 0, st,
+                      (const float *)ws.dacc, anchors, (const float2 *)ws.base.rope, (__nv_bfloat16 *)dc,
+                      (__nv_bfloat16 *)dkr, p.B, p.S, p.N, p.L, p.P);
+}
+
+}  // namespace dspark

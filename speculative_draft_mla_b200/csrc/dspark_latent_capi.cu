@@ -199,8 +199,16 @@ dspark_status dspark_latent_attn_bwd(const dspark_latent_problem *pp, const void
     cudaStream_t st = (cudaStream_t)stream;
     const LatWs w = lat_view(p, workspace);
     if (!(flags & DSPARK_FLAG_REUSE_DESCRIPTOR)) DSPARK_CUDA(launch_build_descriptor(p, anchors, keep, w.base, st));
-    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, nullptr, false, w, st));
-    DSPARK_CUDA(launch_lat_bwd_simt(p, q, c, anchors, keep, lse, do_, dq, dc, dkr, w, st));
+    const bool tc = lat_bwd_tc_supported(p);
+    PadRows pad{};
+    pad.t[0] = dq;
+    pad.rows[0] = p.R;
+    pad.width[0] = p.dqk;
+    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, tc ? &pad : nullptr, tc, w, st));
+    if (tc)
+        DSPARK_CUDA(launch_lat_bwd_tc(p, q, c, anchors, lse, do_, dq, dc, dkr, w, st));
+    else
+        DSPARK_CUDA(launch_lat_bwd_simt(p, q, c, anchors, keep, lse, do_, dq, dc, dkr, w, st));
     return DSPARK_OK;
 }
 

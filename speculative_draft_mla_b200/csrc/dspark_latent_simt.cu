@@ -364,8 +364,6 @@ template <typename T, int KIND> cudaError_t paged_t(const Paged &p, cudaStream_t
 
 }  // namespace
 
-bool lat_bwd_tc_supported(const Prob &p) { return false; }
-
 cudaError_t launch_lat_fwd_simt(const Prob &p, const void *q, const void *c, const int32_t *anchors,
                                 const uint8_t *keep, void *o, float *lse, const LatWs &ws, cudaStream_t st) {
     if (p.dtype == DSPARK_F32)

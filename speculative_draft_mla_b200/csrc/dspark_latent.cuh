@@ -20,7 +20,7 @@ struct LatWsLayout {
     size_t fwd_total;
     size_t dvec;   // float [B, n_h, 5N]: D = sum_k P dP (CUDA-core backward)
     size_t dacc;   // float [B, L, d_l + d_r]: key gradients (tensor-core backward)
-    size_t q_rot;  // bf16 [B, n_h, 5N, d_r]: turned rope queries (tensor-core backward)
+    size_t q_rot;  // bf16 [B, n_h, 5N, 2 d_r]: turned rope queries, hi and lo (tensor-core backward)
     size_t total;
 };
 
@@ -41,7 +41,7 @@ inline LatWsLayout lat_layout(const Prob &p) {
     const bool tc = lat_bwd_tc_supported(p);
     w.dvec = off;      off = align256(off + (tc ? 0 : sizeof(float) * (size_t)p.B * p.n_h * p.R));
     w.dacc = off;      off = align256(off + (tc ? sizeof(float) * (size_t)p.B * p.L * p.dqk : 0));
-    w.q_rot = off;     off = align256(off + (tc ? 2 * (size_t)p.B * p.n_h * p.R * p.d_r : 0));
+    w.q_rot = off;     off = align256(off + (tc ? 4 * (size_t)p.B * p.n_h * p.R * p.d_r : 0));
     w.total = off;
     return w;
 }

@@ -26,8 +26,9 @@
 //
 // Sums of key gradients are fp32 in whatever order the tiles finish: two runs
 // may differ in the last bits before the rounding to bf16. P and dS are bf16
-// operands, the rope slices of Q and K one bf16 each (the gradients are bf16;
-// the forward's LSE is formed more exactly).
+// operands (an error of half a step each, as of the rounded results). The turned
+// rope slices of Q and K are hi + lo of two bf16 in S, as in the forward, and Q's
+// in its product with dS: one bf16 would nearly double the error of dkr.
 //
 // TMEM: S 0..143, dP 144..287, three product buffers 288..479, dd 480..511.
 // Warps 0-7 softmax (warps w and w + 4 share 32 rows, 64 context keys each);
@@ -47,7 +48,8 @@ constexpr int kDL = 512, kDR = 64, kDK = kDL + kDR;
 constexpr int kSlices = 9;
 constexpr int kKeys = 144, kKSlot = kKeys * 128, kKSlots = 4;
 constexpr int kHeads = 22, kRows = 112;            // rows of a tile, padded to the K steps of 16
-constexpr int kSlot = kRows * 128, kPair = 2 * kSlot, kPairs2 = 3;  // Q slice, dO slice
+// Q and dO slices of the same columns; last, hi and lo of Q's rope slice
+constexpr int kSlot = kRows * 128, kPair = 2 * kSlot, kPairs2 = 3;
 constexpr int oK = 0, oPair = kKSlots * kKSlot;
 constexpr int oDS = oPair + kPairs2 * kPair;       // dS, context keys: two slices of 64 keys
 constexpr int oPr = oDS + 2 * kSlot;               // P
@@ -134,8 +136,9 @@ struct TileCursor {
 __global__ void __launch_bounds__(kThreads, 1)
     k_lat_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
                  const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_c,
-                 const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_c5,
-                 const __grid_constant__ CUtensorMap tm_h5, const Args p) {
+                 const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_l,
+                 const __grid_constant__ CUtensorMap tm_c5, const __grid_constant__ CUtensorMap tm_h5,
+                 const __grid_constant__ CUtensorMap tm_l5, const Args p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + kKSlots;
@@ -192,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *dst = sm + oK + s * kKSlot;
                 const int x = c < 8 ? 64 * c : 0;
                 mbar_arrive_expect_tx(&kfull[s], bytes);
-                if (p.W > 1) tma_load_3d(dst, c < 8 ? &tm_c : &tm_h, &kfull[s], x, t.a - (p.W - 1), t.b);
-                tma_load_3d(dst + p.ctxpad * 128, c < 8 ? &tm_c5 : &tm_h5, &kfull[s], x, p.S + kBlock * t.n, t.b);
+                if (p.W > 1) tma_load_3d(dst, c < 8 ? &tm_c : c == 8 ? &tm_h : &tm_l, &kfull[s], x, t.a - (p.W - 1), t.b);
+                tma_load_3d(dst + p.ctxpad * 128, c < 8 ? &tm_c5 : c == 8 ? &tm_h5 : &tm_l5, &kfull[s], x,
+                            p.S + kBlock * t.n, t.b);
                 n_issued++;
                 return true;
             };
@@ -203,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (hp) ok = load(prev, c);
                     if (ok && has && (!hp || cur.fresh)) ok = load(cur, c);
                 }
+                if (ok && has) ok = load(cur, 9);  // the rope keys' lo
                 if (!ok || !has) break;
                 prev = cur;
                 hp = true;
@@ -220,12 +225,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n_issued >= kPairs2 && !mbar_wait(&qempty[s], (n_issued / kPairs2 - 1) & 1, abort_flag, wlim))
                     return false;
                 uint8_t *dst = sm + oPair + s * kPair;
-                mbar_arrive_expect_tx(&qfull[s], c < 8 ? 2 * bytes : bytes);
+                mbar_arrive_expect_tx(&qfull[s], 2 * bytes);
                 if (c < 8) {
                     tma_load_4d(dst, &tm_q, &qfull[s], 64 * c, kBlock * t.n, t.h0, t.b);
                     tma_load_4d(dst + kSlot, &tm_g, &qfull[s], 64 * c, kBlock * t.n, t.h0, t.b);
                 } else {
                     tma_load_4d(dst, &tm_qr, &qfull[s], 0, kBlock * t.n, t.h0, t.b);
+                    tma_load_4d(dst + kSlot, &tm_qr, &qfull[s], 64, kBlock * t.n, t.h0, t.b);
                 }
                 n_issued++;
                 return true;
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const SDesc dda = sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 32 * 128, 1024));   // rows x draft keys
             const SDesc ddb = sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 16, 1024));         // draft keys x rows
             TileCursor cu(p);
-            Tile cur, prev;
+            Tile cur;
             bool ok = true, hp = false;
             uint32_t kn = 0, qn = 0, i = 0, k = 0;  // slots taken; slices of gradients; steps
             auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t d = tmem + kColC + 64 * buf;
                             for (int s = 0; s < ksr; s++) {
                                 mma_bf16_ss(d, dst.at(128 * s), qb.at(128 * s), idK, s > 0);
-                                if (c < 8) mma_bf16_ss(d, pt.at(128 * s), gb.at(128 * s), idK, 1u);
+                                mma_bf16_ss(d, (c < 8 ? pt : dst).at(128 * s), gb.at(128 * s), idK, 1u);
                             }
                             mma_commit(&cfull[3 + buf]);
                         }
@@ -315,21 +321,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
                         const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), 16, 1024));
                         const SDesc gd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), 16, 1024));
+                        // the second product: dP; of the rope slice, S again with Q's lo
+                        const uint32_t d2 = tmem + (c < 8 ? kColP : kColS);
 #pragma unroll
                         for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
-                        if (c < 8) {
 #pragma unroll
-                            for (int s = 0; s < 4; s++)
-                                mma_bf16_ss(tmem + kColP, gd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
+                        for (int s = 0; s < 4; s++) mma_bf16_ss(d2, gd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
+                        mma_commit(&kempty[ks]);
+                        if (c == 8) {  // Q's hi with the keys' lo
+                            ks = kn++ % kKSlots;
+                            if (!wait(&kfull[ks], ((kn - 1) / kKSlots) & 1)) break;
+                            tc_fence_after();
+                            const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
+#pragma unroll
+                            for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), ld.at(2 * s), idS, 1u);
+                            mma_commit(&kempty[ks]);
                         }
                         mma_commit(&qempty[qs]);
                         qn++;
-                        mma_commit(&kempty[ks]);
                     }
                 }
                 if (!ok || !has) break;
                 mma_commit(sfull);
-                prev = cur;
                 hp = true;
             }
         }
@@ -412,21 +425,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 red2(dst + 8 * g, v[s >> 1][4 * g + 2 * (s & 1)], v[s >> 1][4 * g + 2 * (s & 1) + 1]);
                         }
                     }
-                    // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20)
+                    // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20);
+                    // of the rope slice, lanes 64 - 127 its lo's share of dS_d
                     ok = warp_all(mbar_wait(dfull, i & 1, abort_flag, wlim));
                     if (!ok) break;
                     tc_fence_after();
                     float d[8];
-                    tmem_ld8(trow + kColD + (q4 >= 2 ? 16 : 0), d);
+                    tmem_ld8(trow + kColD + (q4 >= 2 && c < 8 ? 16 : 0), d);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(dfree);
-                    if (q4 < 2 || c < 8) {
-                        float *dst = base + (size_t)(p.S + kBlock * prev.n) * kDK + 64 * c + (r & 63);
+                    float *dst = base + (size_t)(p.S + kBlock * prev.n) * kDK + 64 * c + (r & 63);
 #pragma unroll
-                        for (int e = 0; e < kBlock; e++) red1(dst + (size_t)e * kDK, d[e]);
-                    }
+                    for (int e = 0; e < kBlock; e++) red1(dst + (size_t)e * kDK, d[e]);
                 }
             }
             if (!ok || !has) break;
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
 }
 
-// The queries' rope slices turned to their positions (one bf16 each), and the
+// The queries' rope slices turned to their positions, hi then lo, and the
 // key gradients' accumulators cleared.
 __global__ void __launch_bounds__(256) k_lat_bwd_prep(const __nv_bfloat16 *__restrict__ q,
                                                       const int32_t *__restrict__ anchors,
@@ -565,12 +577,17 @@ __global__ void __launch_bounds__(256) k_lat_bwd_prep(const __nv_bfloat16 *__res
         const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + row * kDK + kDL) + u);
         const float4 *cs = reinterpret_cast<const float4 *>(tab + (size_t)pos * (kDR / 2)) + 2 * u;
         const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
-        auto turn = [](uint32_t w, float c, float s) {
+        uint4 hi, lo;
+        auto turn = [](uint32_t w, float c, float s, uint32_t &h, uint32_t &l) {
             const float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xffff0000u);
-            return pack_bf16x2(a * c - b * s, a * s + b * c);
+            split_bf16x2(a * c - b * s, a * s + b * c, h, l);
         };
-        reinterpret_cast<uint4 *>(out + row * kDR)[u] =
-            make_uint4(turn(v.x, c0.x, c0.y), turn(v.y, c0.z, c0.w), turn(v.z, c1.x, c1.y), turn(v.w, c1.z, c1.w));
+        turn(v.x, c0.x, c0.y, hi.x, lo.x);
+        turn(v.y, c0.z, c0.w, hi.y, lo.y);
+        turn(v.z, c1.x, c1.y, hi.z, lo.z);
+        turn(v.w, c1.z, c1.w, hi.w, lo.w);
+        reinterpret_cast<uint4 *>(out + row * 2 * kDR)[u] = hi;
+        reinterpret_cast<uint4 *>(out + row * 2 * kDR + kDR)[u] = lo;
     }
 }
 
@@ -643,11 +660,11 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
         a.err = ws.base.err;
         a.wait_ns = p.wait_ns;
         a.wide = ((uintptr_t)dq & 31) == 0;
-        CUtensorMap mq, mg, mr, mc, mh, mc5, mh5;
+        CUtensorMap mq, mg, mr, mc, mh, ml, mc5, mh5, ml5;
         const uint64_t L = p.L, B = p.B, R = p.R, H = p.n_h;
         const uint64_t qd[4] = {kDK, R, H, B}, qs[3] = {kDK * 2, R * kDK * 2, H * R * kDK * 2};
         const uint64_t gd[4] = {kDL, R, H, B}, gs[3] = {kDL * 2, R * kDL * 2, H * R * kDL * 2};
-        const uint64_t sd[4] = {kDR, R, H, B}, ss[3] = {kDR * 2, R * kDR * 2, H * R * kDR * 2};
+        const uint64_t sd[4] = {2 * kDR, R, H, B}, ss[3] = {kDR * 4, R * kDR * 4, H * R * kDR * 4};
         const uint32_t qb[4] = {64, kBlock, (uint32_t)a.hp, 1};
         const uint64_t cd[3] = {kDL, L, B}, cs[2] = {kDL * 2, L * kDL * 2};
         const uint64_t rd[3] = {kDR, L, B}, rs[2] = {kDR * 2, L * kDR * 2};
@@ -655,13 +672,14 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
         if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mg, dout, 4, gd, gs, qb) ||
             !make_map_nd(&mr, ws.q_rot, 4, sd, ss, qb) || !make_map_nd(&mc, c, 3, cd, cs, wb) ||
             !make_map_nd(&mh, ws.kr_hi, 3, rd, rs, wb) || !make_map_nd(&mc5, c, 3, cd, cs, db) ||
-            !make_map_nd(&mh5, ws.kr_hi, 3, rd, rs, db))
+            !make_map_nd(&mh5, ws.kr_hi, 3, rd, rs, db) || !make_map_nd(&ml, ws.kr_lo, 3, rd, rs, wb) ||
+            !make_map_nd(&ml5, ws.kr_lo, 3, rd, rs, db))
             return cudaErrorInvalidValue;
         e = cudaFuncSetAttribute(k_lat_bwd_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         count_launch();
-        e = launch_pdl(k_lat_bwd_tc, dim3(std::min(a.n_work, nsm)), dim3(kThreads), kSmem, st, mq, mg, mr, mc, mh, mc5,
-                       mh5, a);
+        e = launch_pdl(k_lat_bwd_tc, dim3(std::min(a.n_work, nsm)), dim3(kThreads), kSmem, st, mq, mg, mr, mc, mh, ml,
+                       mc5, mh5, ml5, a);
         if (e != cudaSuccess) return e;
     }
     count_launch();

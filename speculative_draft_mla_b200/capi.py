@@ -351,27 +351,55 @@ def alloc_latent_workspace(prob, device):
 
 
 def _same(name, t, shape, dtype, device):
+    """t is a contiguous CUDA tensor of this shape, type and device."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous() and t.is_cuda:
+        return
     if t.dtype != dtype:
         raise TypeError("%s must be %s" % (name, dtype))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if t.device != device:
         raise ValueError("%s is on %s, not %s" % (name, t.device, device))
+    _cuda(t)
+
+
+def _ws_ok(ws, device):
+    if not (ws.is_cuda and ws.dtype is torch.uint8 and ws.device == device and ws.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on %s" % device)
+
+
+def _call(name, device, stream, *args):
+    """The entry point on the tensors' device and, unless one is given, its current stream (the last argument)."""
+    f = getattr(_lib or load(), name)
+    at = device.index
+    if torch._C._cuda_getDevice() == at:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    if status:
+        raise DsparkError(status, name)
+
+
+def _at(t):
+    return t.data_ptr() or None  # (an empty tensor has no address)
 
 
 def _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base):
-    _cuda(q, c, kr, anchors, keep)
+    if not q.is_cuda or not q.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
     if q.dim() != 4 or c.dim() != 3 or kr.dim() != 3 or q.shape[2] % 5:
         raise ValueError("q [B, n_h, 5N, d_l + d_r], c [B, S + 5N, d_l], kr [B, S + 5N, d_r]")
     B, n_h, R, dk = q.shape
     d_l, d_r = c.shape[2], kr.shape[2]
     if dk != d_l + d_r:
         raise ValueError("q is %d wide, c and kr %d + %d" % (dk, d_l, d_r))
-    _same("c", c, (B, S + R, d_l), q.dtype, q.device)
-    _same("kr", kr, (B, S + R, d_r), q.dtype, q.device)
-    _same("anchors", anchors, (B, R // 5), torch.int32, q.device)
-    _same("keep", keep, (B, R // 5), torch.uint8, q.device)
-    return latent_problem(B, n_h, S, R // 5, W, d_l, d_r, scale, rope_base, dtype_code(q.dtype))
+    dt, dev = q.dtype, q.device
+    _same("c", c, (B, S + R, d_l), dt, dev)
+    _same("kr", kr, (B, S + R, d_r), dt, dev)
+    _same("anchors", anchors, (B, R // 5), torch.int32, dev)
+    _same("keep", keep, (B, R // 5), torch.uint8, dev)
+    return latent_problem(B, n_h, S, R // 5, W, d_l, d_r, scale, rope_base, dtype_code(dt))
 
 
 def latent_attn_fwd(q, c, kr, anchors, keep, S, W, scale=LATENT_SCALE, rope_base=10000.0, workspace=None, flags=0,
@@ -379,19 +407,19 @@ def latent_attn_fwd(q, c, kr, anchors, keep, S, W, scale=LATENT_SCALE, rope_base
     """Draft attention over latents: q [B, n_h, 5N, d_l + d_r], c [B, S + 5N, d_l], kr [B, S + 5N, d_r].
     Returns (o [B, n_h, 5N, d_l], lse, workspace). ``out`` may pass preallocated (o, lse)."""
     prob = _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base)
+    dev, rows = q.device, tuple(q.shape[:3])
     if workspace is None:
-        workspace = alloc_latent_workspace(prob, q.device)
+        workspace = alloc_latent_workspace(prob, dev)
     if out is None:
-        out = (torch.empty(q.shape[:3] + (c.shape[2],), dtype=q.dtype, device=q.device),
-               torch.empty(q.shape[:3], dtype=torch.float32, device=q.device))
-    o, lse = out
-    _cuda(o, lse, workspace)
-    _same("o", o, q.shape[:3] + (c.shape[2],), q.dtype, q.device)
-    _same("lse", lse, q.shape[:3], torch.float32, q.device)
-    with torch.cuda.device(q.device):
-        _check(load().dspark_latent_attn_fwd(ctypes.byref(prob), _ptr(q), _ptr(c), _ptr(kr), _ptr(anchors), _ptr(keep),
-                                             _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), flags,
-                                             _stream(stream, q.device)), "dspark_latent_attn_fwd")
+        o = torch.empty(rows + (prob.d_l,), dtype=q.dtype, device=dev)
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        o, lse = out
+        _same("o", o, rows + (prob.d_l,), q.dtype, dev)
+        _same("lse", lse, rows, torch.float32, dev)
+    _ws_ok(workspace, dev)
+    _call("dspark_latent_attn_fwd", dev, stream, ctypes.byref(prob), _at(q), _at(c), _at(kr), _at(anchors), _at(keep),
+          _at(o), _at(lse), _at(workspace), workspace.numel(), flags)
     return o, lse, workspace
 
 
@@ -400,21 +428,20 @@ def latent_attn_bwd(q, c, kr, anchors, keep, lse, dout, S, W, scale=LATENT_SCALE
     """Returns (dq, dc, dkr) for dL/dO = dout and the forward's lse (its O is not needed). ``out`` may pass
     preallocated gradients."""
     prob = _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base)
+    dev, rows = q.device, tuple(q.shape[:3])
     if workspace is None:
-        workspace = alloc_latent_workspace(prob, q.device)
+        workspace = alloc_latent_workspace(prob, dev)
+    _same("lse", lse, rows, torch.float32, dev)
+    _same("dout", dout, rows + (prob.d_l,), q.dtype, dev)
     if out is None:
-        out = (torch.empty_like(q), torch.empty_like(c), torch.empty_like(kr))
-    dq, dc, dkr = out
-    _cuda(lse, dout, dq, dc, dkr, workspace)
-    _same("lse", lse, q.shape[:3], torch.float32, q.device)
-    _same("dout", dout, q.shape[:3] + (c.shape[2],), q.dtype, q.device)
-    for name, g, x in (("dq", dq, q), ("dc", dc, c), ("dkr", dkr, kr)):
-        _same(name, g, x.shape, q.dtype, q.device)
-    with torch.cuda.device(q.device):
-        _check(load().dspark_latent_attn_bwd(ctypes.byref(prob), _ptr(q), _ptr(c), _ptr(kr), _ptr(anchors), _ptr(keep),
-                                             _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dc), _ptr(dkr), _ptr(workspace),
-                                             workspace.numel(), flags, _stream(stream, q.device)),
-               "dspark_latent_attn_bwd")
+        dq, dc, dkr = torch.empty_like(q), torch.empty_like(c), torch.empty_like(kr)
+    else:
+        dq, dc, dkr = out
+        for name, g, x in (("dq", dq, q), ("dc", dc, c), ("dkr", dkr, kr)):
+            _same(name, g, x.shape, q.dtype, dev)
+    _ws_ok(workspace, dev)
+    _call("dspark_latent_attn_bwd", dev, stream, ctypes.byref(prob), _at(q), _at(c), _at(kr), _at(anchors), _at(keep),
+          _at(lse), _at(dout), _at(dq), _at(dc), _at(dkr), _at(workspace), workspace.numel(), flags)
     return dq, dc, dkr
 
 
@@ -422,15 +449,18 @@ def latent_row_bytes(kind, d_l, d_r):
     return int(load().dspark_latent_row_bytes(int(kind), int(d_l), int(d_r)))
 
 
+_KINDS = {torch.float32: CACHE_F32, torch.bfloat16: CACHE_BF16, torch.uint8: CACHE_FP8}
+
+
 def _cache_kind(cache, d_l, d_r):
     """Kind of a cache tensor [n_pages, page_size, row]: float32 / bfloat16 rows of d_l + d_r values, or the
     bytes (uint8) of the 8-bit kind."""
-    kinds = {torch.float32: CACHE_F32, torch.bfloat16: CACHE_BF16, torch.uint8: CACHE_FP8}
-    _cuda(cache)
-    if cache.dim() != 3 or cache.dtype not in kinds:
+    kind = _KINDS.get(cache.dtype)
+    if kind is None or cache.dim() != 3:
         raise ValueError("cache must be [n_pages, page_size, row] of float32, bfloat16 or uint8 (the 8-bit kind)")
-    kind = kinds[cache.dtype]
-    if cache.shape[2] * cache.element_size() != latent_row_bytes(kind, d_l, d_r):
+    if not cache.is_cuda or not cache.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if cache.shape[2] * cache.itemsize != latent_row_bytes(kind, d_l, d_r):
         raise ValueError("cache rows of %d elements do not fit d_l = %d, d_r = %d" % (cache.shape[2], d_l, d_r))
     return kind
 
@@ -447,38 +477,32 @@ def latent_cache(n_pages, page_size, d_l=512, d_r=64, kind=CACHE_BF16, device="c
 def latent_cache_write(cache, c, kr, positions, slots, norm_weight=None, eps=1e-5, rope_base=10000.0, stream=None):
     """Writes T tokens' latents c [T, d_l] (RMS-normed when norm_weight [d_l] is given) and rope keys kr [T, d_r]
     (turned to positions [T] int32) into rows slots [T] int64 of the cache; a slot out of range writes nothing."""
-    _cuda(c, kr, positions, slots, norm_weight)
     if c.dim() != 2 or kr.dim() != 2:
         raise ValueError("c [T, d_l], kr [T, d_r]")
     T, d_l = c.shape
-    kind = _cache_kind(cache, d_l, kr.shape[1])
-    dev = cache.device
-    _same("c", c, (T, d_l), c.dtype, dev)
-    _same("kr", kr, (T, kr.shape[1]), c.dtype, dev)
+    d_r, dt, dev = kr.shape[1], c.dtype, cache.device
+    kind = _cache_kind(cache, d_l, d_r)
+    _same("c", c, (T, d_l), dt, dev)
+    _same("kr", kr, (T, d_r), dt, dev)
     _same("positions", positions, (T,), torch.int32, dev)
     _same("slots", slots, (T,), torch.int64, dev)
     if norm_weight is not None:
-        _same("norm_weight", norm_weight, (d_l,), c.dtype, dev)
-    prob = LatentCache(T, d_l, kr.shape[1], kind, cache.shape[0], cache.shape[1], dtype_code(c.dtype), 0)
-    with torch.cuda.device(dev):
-        _check(load().dspark_latent_cache_write(ctypes.byref(prob), _ptr(c), _ptr(kr), _ptr(norm_weight), float(eps),
-                                                float(rope_base), _ptr(positions), _ptr(slots), _ptr(cache),
-                                                _stream(stream, dev)), "dspark_latent_cache_write")
+        _same("norm_weight", norm_weight, (d_l,), dt, dev)
+    prob = LatentCache(T, d_l, d_r, kind, cache.shape[0], cache.shape[1], dtype_code(dt), 0)
+    _call("dspark_latent_cache_write", dev, stream, ctypes.byref(prob), _at(c), _at(kr),
+          None if norm_weight is None else _at(norm_weight), float(eps), float(rope_base), _at(positions), _at(slots),
+          _at(cache))
 
 
 def latent_cache_read(cache, slots, d_l=512, d_r=64, dtype=torch.bfloat16, stream=None):
     """Rows slots [T] int64 as the values that they stand for: (c [T, d_l], rotated rope keys [T, d_r])."""
     kind = _cache_kind(cache, d_l, d_r)
-    _cuda(slots)
-    dev = cache.device
-    _same("slots", slots, (slots.numel(),), torch.int64, dev)
-    T = slots.numel()
-    c = torch.empty(T, d_l, dtype=dtype, device=dev)
-    kr = torch.empty(T, d_r, dtype=dtype, device=dev)
+    dev, T = cache.device, slots.numel()
+    _same("slots", slots, (T,), torch.int64, dev)
+    c = torch.empty((T, d_l), dtype=dtype, device=dev)
+    kr = torch.empty((T, d_r), dtype=dtype, device=dev)
     prob = LatentCache(T, d_l, d_r, kind, cache.shape[0], cache.shape[1], dtype_code(dtype), 0)
-    with torch.cuda.device(dev):
-        _check(load().dspark_latent_cache_read(ctypes.byref(prob), _ptr(cache), _ptr(slots), _ptr(c), _ptr(kr),
-                                               _stream(stream, dev)), "dspark_latent_cache_read")
+    _call("dspark_latent_cache_read", dev, stream, ctypes.byref(prob), _at(cache), _at(slots), _at(c), _at(kr))
     return c, kr
 
 
@@ -486,18 +510,20 @@ def _paged(q, cache, block_table, max_kv_len, d_l, d_r, scale, causal, window, r
     kind = _cache_kind(cache, d_l, d_r)
     if not q.is_cuda or q.dim() != 3 or q.shape[2] != d_l + d_r:
         raise ValueError("q must be a CUDA tensor [T, n_h, d_l + d_r]")
-    for name, t in (("q", q), ("o", o)):
-        if t is not None and t.numel() and t.stride(2) != 1:
-            raise ValueError("%s must be contiguous in its last dimension" % name)
-    _cuda(block_table)
     T, n_h = q.shape[:2]
 
-    def strides(t):
-        return (0, 0) if t is None or t.numel() == 0 else (t.stride(0), t.stride(1))
+    def strides(name, t):
+        if t is None or t.numel() == 0:
+            return 0, 0
+        a, b, c = t.stride()
+        if c != 1:
+            raise ValueError("%s must be contiguous in its last dimension" % name)
+        return a, b
 
-    return LatentPaged(block_table.shape[0], T, n_h, d_l, d_r, cache.shape[1], cache.shape[0], block_table.shape[1],
-                       int(max_kv_len), int(window), int(bool(causal)), dtype_code(q.dtype), kind, 0, *strides(q),
-                       *strides(o), float(rope_base), float(scale))
+    n_seq, max_pages = block_table.shape
+    return LatentPaged(n_seq, T, n_h, d_l, d_r, cache.shape[1], cache.shape[0], max_pages, int(max_kv_len), int(window),
+                       int(bool(causal)), dtype_code(q.dtype), kind, 0, *strides("q", q), *strides("o", o),
+                       float(rope_base), float(scale))
 
 
 def latent_paged_workspace_size(prob):
@@ -519,25 +545,25 @@ def latent_attn_paged(q, cache, block_table, q_start, kv_len, max_kv_len=0, d_l=
     [n_seq + 1], kv_len [n_seq] and block_table [n_seq, max_pages] int32. causal=False is a draft block whose
     tokens see one another. Returns (o [T, n_h, d_l], lse [T, n_h], workspace); rows behind the last sequence are
     left as they were in ``out`` and are unspecified otherwise."""
-    o, lse = out if out is not None else (None, None)
-    if o is None:
-        o = torch.empty(q.shape[0], q.shape[1], d_l, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
+    dev, T, n_h = q.device, q.shape[0], q.shape[1]
+    if out is None:
+        o = torch.empty((T, n_h, d_l), dtype=q.dtype, device=dev)
+        lse = torch.empty((T, n_h), dtype=torch.float32, device=dev)
+    else:
+        o, lse = out
+        if o.shape != (T, n_h, d_l) or o.dtype != q.dtype or o.device != dev:
+            raise ValueError("o must be [T, n_h, d_l] like q")
+        _same("lse", lse, (T, n_h), torch.float32, dev)
     prob = _paged(q, cache, block_table, max_kv_len, d_l, d_r, scale, causal, window, rope_base, o)
-    _cuda(q_start, kv_len, lse)
-    n_seq, dev = block_table.shape[0], q.device
     if cache.device != dev:
         raise ValueError("cache is on %s, not %s" % (cache.device, dev))
-    _same("block_table", block_table, block_table.shape, torch.int32, dev)
+    n_seq = prob.n_seq
+    _same("block_table", block_table, (n_seq, prob.max_pages), torch.int32, dev)
     _same("q_start", q_start, (n_seq + 1,), torch.int32, dev)
     _same("kv_len", kv_len, (n_seq,), torch.int32, dev)
-    _same("o", o, (q.shape[0], q.shape[1], d_l), q.dtype, dev)
-    _same("lse", lse, q.shape[:2], torch.float32, dev)
     if workspace is None:
         workspace = torch.empty(max(latent_paged_workspace_size(prob), 256), dtype=torch.uint8, device=dev)
-    _cuda(workspace)
-    with torch.cuda.device(dev):
-        _check(load().dspark_latent_attn_paged(ctypes.byref(prob), _ptr(q), _ptr(cache), _ptr(block_table),
-                                               _ptr(q_start), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(workspace),
-                                               workspace.numel(), _stream(stream, dev)), "dspark_latent_attn_paged")
+    _ws_ok(workspace, dev)
+    _call("dspark_latent_attn_paged", dev, stream, ctypes.byref(prob), _at(q), _at(cache), _at(block_table),
+          _at(q_start), _at(kv_len), _at(o), _at(lse), _at(workspace), workspace.numel())
     return o, lse, workspace

@@ -7,8 +7,14 @@
 
 namespace dspark {
 
+// (a thread's last table is kept: it depends on these two values alone)
 RopeFreq rope_freq(int d_r, double base) {
-    RopeFreq r{};
+    thread_local RopeFreq r{};
+    thread_local int have_d = -1;
+    thread_local double have_base = 0.0;
+    if (d_r == have_d && base == have_base) return r;
+    have_d = d_r;
+    have_base = base;
     for (int i = 0; i < d_r / 2 && i < 64; i++) r.f[i] = std::pow(base, -2.0 * i / d_r);
     return r;
 }

@@ -284,8 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (u > 0 && !wait(&cfree[buf], (u - 1) & 1)) break;
                             tc_fence_after();
                             const uint32_t d = tmem + kColC + 64 * buf;
-                            for (int s = 0; s < ksc; s++)
-                                mma_bf16_ss(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
+                            // (unrolled: a product of 64 columns takes 50 cycles, a step of a rolled loop 90)
+#pragma unroll
+                            for (int s = 0; s < 8; s++)
+                                if (s < ksc) mma_bf16_ss(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
                             mma_bf16_ss(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
                             mma_commit(&cfull[buf]);
                         }
@@ -294,7 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (u > 0 && !wait(&cfree[buf], (u - 1) & 1)) break;
                             tc_fence_after();
                             const uint32_t d = tmem + kColC + 64 * buf;
-                            for (int s = 0; s < ksr; s++) {
+#pragma unroll
+                            for (int s = 0; s < kRows / 16; s++) {
+                                if (s >= ksr) continue;
                                 mma_bf16_ss(d, dst.at(128 * s), qb.at(128 * s), idK, s > 0);
                                 mma_bf16_ss(d, (c < 8 ? pt : dst).at(128 * s), gb.at(128 * s), idK, 1u);
                             }
@@ -302,8 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (i > 0 && !wait(dfree, (i - 1) & 1)) break;
                         tc_fence_after();
-                        for (int s = 0; s < ksr; s++)
-                            mma_bf16_ss(tmem + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
+#pragma unroll
+                        for (int s = 0; s < kRows / 16; s++)
+                            if (s < ksr) mma_bf16_ss(tmem + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
                         mma_commit(&qempty[qs]);
                         if (!has || cur.fresh) mma_commit(&kempty[ks]);
                         mma_commit(dfull);  // last: nothing is in flight once its reader has it

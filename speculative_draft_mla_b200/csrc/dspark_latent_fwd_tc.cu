@@ -25,7 +25,7 @@
 // 288..351, O 352..415 / 416..479.
 // Warps: 0-3 and 4-7 softmax and output of even and odd tiles (thread = row);
 // 8-11 turn the query's rope slice, global -> TMEM; 12 loads Q slices, 13 loads
-// keys, 14 issues the MMAs (one thread each).
+// keys, 14 issues the products of S, 15 those of O (one thread each).
 // Keys of a block: context slot i is position A - W + 1 + i (before the
 // sequence's start: zero fill by TMA), then, at the next multiple of 32, the 5
 // draft keys; no other row of memory is ever read into a slot, the slots
@@ -59,7 +59,7 @@ static_assert(kKSlice % 1024 == 0 && kQSlot % 1024 == 0, "swizzle atoms");
 
 constexpr uint32_t kColS = 0, kColR = 2 * kKeys, kColO = kColR + 64;
 constexpr int kWarpR = 8, kWarpQ = 12, kWarpK = 13, kWarpM = 14;
-constexpr int kThreads = 15 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + kKSlices;
     uint64_t *qfull = kempty + kKSlices, *qempty = qfull + kQSlots;
     uint64_t *sfull = qempty + kQSlots, *pready = sfull + 2, *ofull = pready + 2, *ofree = ofull + 4;
-    uint64_t *rready = ofree + 2, *rfree = rready + 1, *drain = rready + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(drain + 2);
+    uint64_t *pvdone = ofree + 2, *rready = pvdone + 2, *rfree = rready + 1, *drain = rready + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(drain + 3);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t wlim = p.wait_ns;
 
@@ -107,7 +107,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(rready, 4);
         mbar_init(rfree, 1);
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&pvdone[i], 1);
+            mbar_init(&drain[i], 1);
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -173,101 +176,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kWarpM) {
-        // ------------------------------------------------------ MMAs
+        // ------------------------------------------------- S = Q K^T
         if (lane == 0) {
-            const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0), idO = idesc_bf16(128, 64, 1);
-            const int ksteps = p.ctxpad / 16 + 1;
-            // two cursors over the CTA's tiles: S = Q K^T (tile i, slice c) and
-            // P V (tile j, chunk d); whichever has its inputs goes next
-            DraftCursor curp = cur;
-            DraftItem ip;
-            int wq = blockIdx.x, wp = blockIdx.x, tq = 0, tp = 0, c = 0, d = 0;
-            uint32_t i = 0, j = 0, kq = 0;  // tiles; items of the S cursor
-            bool hq = wq < p.n_work && cur.at(wq, it), hp = hq && curp.at(wp, ip), ok = true;
-            if (hq) {
-                tq = it.t0;
-                tp = ip.t0;
-            }
-            uint64_t idle = 0;
-            while (ok && hp) {
-                bool issued = false;
-                if (hq && (c > 0 || i < 2 || j + 2 > i)) {
+            const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0);
+            uint32_t i = 0, g = 0, k = 0;  // tiles, slices, items
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
+            for (int w = blockIdx.x; ok && w < p.n_work && cur.at(w, it); w += G, k++)
+                for (int t = it.t0; ok && t < it.t1; t++, i++) {
+                    if (i >= 2 && !wait(&pvdone[i & 1], ((i >> 1) - 1) & 1)) break;
                     const uint32_t dS = tmem + kColS + (i & 1) * kKeys;
-                    if (c < kSlices) {
-                        const uint32_t g = i * kSlices + c, s = g % kQSlots;
-                        if (mbar_test(&qfull[s], (g / kQSlots) & 1) && mbar_test(&kfull[c], kq & 1)) {
-                            tc_fence_after();
-                            const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oQ + s * kQSlot), 16, 1024));
-                            const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm + c * kKSlice), 16, 1024));
-#pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                mma_bf16_ss(dS, qd.at(2 * k), kd.at(2 * k), idS, (c | k) != 0 ? 1u : 0u);
-                            mma_commit(&qempty[s]);
-                            c++;
-                            issued = true;
-                        }
-                    } else if (mbar_test(rready, i & 1) && mbar_test(&kfull[kSlices], kq & 1) &&
-                               mbar_test(&kfull[kSlices + 1], kq & 1)) {
+#pragma unroll 1
+                    for (int c = 0; c < kSlices; c++, g++) {
+                        const uint32_t s = g % kQSlots;
+                        if ((t == it.t0 && !wait(&kfull[c], k & 1)) || !wait(&qfull[s], (g / kQSlots) & 1)) break;
                         tc_fence_after();
-                        const SDesc hd = sdesc_split(sdesc_sw128(smem_u32(sm + kSlices * kKSlice), 16, 1024));
-                        const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + (kSlices + 1) * kKSlice), 16, 1024));
+                        const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oQ + s * kQSlot), 16, 1024));
+                        const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm + c * kKSlice), 16, 1024));
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            mma_bf16_ts(dS, tmem + kColR + 8 * k, hd.at(2 * k), idS, 1u);
-                            mma_bf16_ts(dS, tmem + kColR + 32 + 8 * k, hd.at(2 * k), idS, 1u);
-                            mma_bf16_ts(dS, tmem + kColR + 8 * k, ld.at(2 * k), idS, 1u);
-                        }
-                        mma_commit(rfree);
-                        mma_commit(&sfull[i & 1]);
-                        c = 0;
-                        i++;
-                        if (++tq == it.t1) {
-                            mma_commit(&kempty[kSlices]);
-                            mma_commit(&kempty[kSlices + 1]);
-                            wq += G;
-                            kq++;
-                            hq = wq < p.n_work && cur.at(wq, it);
-                            if (hq) tq = it.t0;
-                        }
-                        issued = true;
+                        for (int u = 0; u < 4; u++)
+                            mma_bf16_ss(dS, qd.at(2 * u), kd.at(2 * u), idS, (c | u) != 0 ? 1u : 0u);
+                        mma_commit(&qempty[s]);
                     }
+                    if (t == it.t0 && (!wait(&kfull[kSlices], k & 1) || !wait(&kfull[kSlices + 1], k & 1))) break;
+                    if (!wait(rready, i & 1)) break;
+                    tc_fence_after();
+                    const SDesc hd = sdesc_split(sdesc_sw128(smem_u32(sm + kSlices * kKSlice), 16, 1024));
+                    const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + (kSlices + 1) * kKSlice), 16, 1024));
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        mma_bf16_ts(dS, tmem + kColR + 8 * u, hd.at(2 * u), idS, 1u);
+                        mma_bf16_ts(dS, tmem + kColR + 32 + 8 * u, hd.at(2 * u), idS, 1u);
+                        mma_bf16_ts(dS, tmem + kColR + 8 * u, ld.at(2 * u), idS, 1u);
+                    }
+                    mma_commit(rfree);
+                    if (t + 1 == it.t1) {
+                        mma_commit(&kempty[kSlices]);
+                        mma_commit(&kempty[kSlices + 1]);
+                    }
+                    mma_commit(&sfull[i & 1]);  // (last: nothing is in flight once its reader has it)
                 }
-                if (j < i) {
-                    const uint32_t g = j * kSlices + d, s = g & 1;
-                    if ((d > 0 || mbar_test(&pready[j & 1], (j >> 1) & 1)) &&
-                        (g < 2 || mbar_test(&ofree[s], ((g >> 1) - 1) & 1))) {
+        }
+    } else if (warp == kWarpM + 1) {
+        // ------------------------------------------------- O = P V
+        // (an issuer of its own: one thread issuing both was the bound, at twice
+        // the time of the products)
+        if (lane == 0) {
+            const uint32_t idO = idesc_bf16(128, 64, 1);
+            const int ksteps = p.ctxpad / 16 + 1;
+            uint32_t j = 0, g = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
+            for (int w = blockIdx.x; ok && w < p.n_work && cur.at(w, it); w += G)
+                for (int t = it.t0; ok && t < it.t1; t++, j++) {
+                    if (!wait(&pready[j & 1], (j >> 1) & 1)) break;
+                    const uint32_t pa = tmem + kColS + (j & 1) * kKeys;
+#pragma unroll 1
+                    for (int d = 0; d < kSlices; d++, g++) {
+                        const uint32_t s = g & 1, dO = tmem + kColO + 64 * s;
+                        if (g >= 2 && !wait(&ofree[s], ((g >> 1) - 1) & 1)) break;
                         tc_fence_after();
                         const SDesc vd = sdesc_split(sdesc_sw128(smem_u32(sm + d * kKSlice), kKSlice, 1024));
-                        const uint32_t pa = tmem + kColS + (j & 1) * kKeys, dO = tmem + kColO + 64 * s;
-                        for (int k = 0; k < ksteps; k++)
-                            mma_bf16_ts(dO, pa + 8 * k, vd.at(128 * k), idO, k > 0 ? 1u : 0u);
-                        // (the output's barrier last: nothing is in flight once its reader has it)
-                        if (tp + 1 == ip.t1) mma_commit(&kempty[d]);
-                        mma_commit(&ofull[2 * (j & 1) + s]);
-                        if (++d == kSlices) {
-                            d = 0;
-                            j++;
-                            if (++tp == ip.t1) {
-                                wp += G;
-                                hp = wp < p.n_work && curp.at(wp, ip);
-                                if (hp) tp = ip.t0;
-                            }
-                        }
-                        issued = true;
+                        // (unrolled: a product of 64 columns takes 50 cycles, a step of a rolled loop 90)
+#pragma unroll
+                        for (int u = 0; u < kKeys / 16; u++)
+                            if (u < ksteps) mma_bf16_ts(dO, pa + 8 * u, vd.at(128 * u), idO, u > 0 ? 1u : 0u);
+                        if (t + 1 == it.t1) mma_commit(&kempty[d]);
+                        if (d == kSlices - 1) mma_commit(&pvdone[j & 1]);
+                        mma_commit(&ofull[2 * (j & 1) + s]);  // (last)
                     }
                 }
-                if (issued) {
-                    idle = 0;
-                } else {
-                    const uint64_t now = globaltimer();
-                    if (idle == 0) idle = now;
-                    if (*abort_flag) ok = false;
-                    else if (now - idle > wlim) {
-                        *abort_flag = 1;
-                        ok = false;
-                    }
-                }
-            }
         }
     } else if (warp >= kWarpR) {
         // ------------------------------- rope slice of the queries -> TMEM
@@ -326,14 +304,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // the block's keys: context slots [lo, W - 1), draft slots 0 .. 4
                 const int lo = max(0, p.W - 1 - it.a), hi = p.W - 1;
+                // (chunks of 32 slots that are visible throughout take no tests)
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 for (int c = 0; c < p.ctxpad; c += 32) {
                     float s[32];
                     tmem_ld32(tS + c, s);
                     tmem_wait_ld();
+                    if (c >= lo && c + 32 <= hi) {
 #pragma unroll
-                    for (int k = 0; k < 32; k++)
-                        if (c + k >= lo && c + k < hi) m[k & 3] = fmaxf(m[k & 3], s[k]);
+                        for (int k = 0; k < 32; k++) m[k & 3] = fmaxf(m[k & 3], s[k]);
+                    } else {
+                        const uint32_t in = slot_mask(lo - c, hi - c);
+#pragma unroll
+                        for (int k = 0; k < 32; k++) m[k & 3] = fmaxf(m[k & 3], (in >> k) & 1 ? s[k] : -INFINITY);
+                    }
                 }
                 float sd[8];
                 tmem_ld8(tS + p.ctxpad, sd);
@@ -348,10 +332,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float s[32];
                     tmem_ld32(tS + c, s);
                     tmem_wait_ld();
+                    if (!(c >= lo && c + 32 <= hi)) {
+                        const uint32_t in = slot_mask(lo - c, hi - c);
+#pragma unroll
+                        for (int k = 0; k < 32; k++) s[k] = (in >> k) & 1 ? s[k] : -INFINITY;
+                    }
                     uint32_t pw[16];
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
-                        s[k] = c + k >= lo && c + k < hi ? ex2(fmaf(s[k], p.scale_log2, neg)) : 0.f;
+                        s[k] = ex2(fmaf(s[k], p.scale_log2, neg));
                         l[k & 3] += s[k];
                     }
 #pragma unroll
@@ -419,9 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t n = issued_k[0] + (c < issued_k[1] ? 1u : 0u);
                 if (n) mbar_wait(&kfull[c], (n - 1) & 1, &never);
             }
-        if (warp == kWarpM) {
-            mma_commit(drain);
-            mbar_wait(drain, 0, &never);
+        if (warp >= kWarpM) {
+            mma_commit(&drain[warp - kWarpM]);
+            mbar_wait(&drain[warp - kWarpM], 0, &never);
         }
     }
     tc_fence_before();

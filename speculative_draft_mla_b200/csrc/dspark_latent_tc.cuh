@@ -30,6 +30,11 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, uin
         "l"((uint64_t)m), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
+// Bits [lo, hi) of 32 (both may lie outside).
+__device__ __forceinline__ uint32_t slot_mask(int lo, int hi) {
+    if (hi <= 0 || lo >= 32 || hi <= lo) return 0u;
+    return (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & ~(lo <= 0 ? 0u : (1u << lo) - 1u);
+}
 // 32 bytes to global memory: one store where the address allows it.
 __device__ __forceinline__ void st_global_32B(void *p, const uint32_t (&v)[8], bool wide) {
     if (wide) {

@@ -30,10 +30,10 @@
 // rope slices of Q and K are hi + lo of two bf16 in S, as in the forward, and Q's
 // in its product with dS: one bf16 would nearly double the error of dkr.
 //
-// TMEM: S 0..143, dP 144..287, three product buffers 288..479, dd 480..511.
+// TMEM: S 0..143, dP 144..287, dq 288..351, dk 352..415 / 416..479, dd 480..511.
 // Warps 0-7 softmax (warps w and w + 4 share 32 rows, 64 context keys each);
-// 0-3 then store dq, 4-7 reduce dk and dd; 8 loads keys, 9 Q and dO, 10 issues
-// the MMAs. Every wait is bounded.
+// 0-3 then store dq, 4-7 reduce dk and dd; 8 loads keys, 9 Q and dO, 10 - 12
+// issue the MMAs. Every wait is bounded.
 #include <algorithm>
 
 #include "dspark_latent_tc.cuh"
@@ -60,7 +60,7 @@ constexpr int kSmem = oBar + 512 + 1024;
 static_assert(kHeads * kBlock <= kRows && kSmem <= 232448, "shared memory");
 static_assert(kSlot % 1024 == 0 && oDD % 1024 == 0, "swizzle atoms");
 constexpr uint32_t kColS = 0, kColP = kKeys, kColC = 2 * kKeys, kColD = kColC + 3 * 64;
-constexpr int kWarpK = 8, kWarpQ = 9, kWarpM = 10, kThreads = 11 * 32;
+constexpr int kWarpK = 8, kWarpQ = 9, kWarpM = 10, kThreads = 13 * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -77,8 +77,8 @@ struct Args {
     bool wide;
 };
 
-__device__ __forceinline__ void red2(float *a, float x, float y) {
-    asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(a), "f"(x), "f"(y) : "memory");
+__device__ __forceinline__ void red4(float *a, float x, float y, float z, float w) {
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 __device__ __forceinline__ void red1(float *a, float x) {
     asm volatile("red.global.add.f32 [%0], %1;" ::"l"(a), "f"(x) : "memory");
@@ -100,7 +100,10 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
 }
 
-// The CTA's tiles in order, over its items.
+// The CTA's tiles in order, over its items: a run of neighbouring blocks, so
+// that CTAs at work at the same time add to different keys (with blocks dealt
+// out in turn, 16 CTAs met on the same keys and the reductions took four times
+// as long).
 struct Tile {
     int b, n, a, h0, nh;
     bool fresh;  // first of its item: other keys than the tile before
@@ -108,15 +111,20 @@ struct Tile {
 struct TileCursor {
     DraftCursor cur;
     DraftItem it;
-    int w, t, G;
+    int w, w1, t;
     bool open;
     __device__ __forceinline__ TileCursor(const Args &p)
-        : cur{p.cnt, p.sorted_n, p.sorted_a, p.B, p.N, p.nsplit, p.tiles, p.per}, w(blockIdx.x), t(0),
-          G(gridDim.x), open(false) {}
+        : cur{p.cnt, p.sorted_n, p.sorted_a, p.B, p.N, p.nsplit, p.tiles, p.per}, t(0), open(false) {
+        long long n = 0;
+        for (int b = 0; b < p.B; b++) n += p.cnt[b];
+        n *= p.nsplit;
+        w = (int)(n * blockIdx.x / gridDim.x);
+        w1 = (int)(n * (blockIdx.x + 1) / gridDim.x);
+    }
     __device__ __forceinline__ bool next(const Args &p, Tile &o) {
         o.fresh = !open;
         if (!open) {
-            if (w >= p.n_work || !cur.at(w, it)) return false;
+            if (w >= w1 || !cur.at(w, it)) return false;
             t = it.t0;
             open = true;
         }
@@ -127,7 +135,7 @@ struct TileCursor {
         o.nh = min(p.hp, p.n_h - o.h0);
         if (++t == it.t1) {
             open = false;
-            w += G;
+            w++;
         }
         return true;
     }
@@ -141,10 +149,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tm_l5, const Args p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + kKSlots;
-    uint64_t *qfull = kempty + kKSlots, *qempty = qfull + kPairs2;
+    // a slot's full barriers: [0] of copies for the gradients, [1] of those for the scores
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + 2 * kKSlots;
+    uint64_t *qfull = kempty + kKSlots, *qempty = qfull + 2 * kPairs2;
     uint64_t *sfull = qempty + kPairs2, *pds = sfull + 1, *drain = sfull + 2;
-    uint64_t *cfull = sfull + 3, *cfree = cfull + 6, *dfull = cfree + 3, *dfree = dfull + 1, *lbar = dfull + 2;
+    uint64_t *qcfull = sfull + 5, *qcfree = qcfull + 1, *kcfull = qcfull + 2, *kcfree = kcfull + 2;
+    uint64_t *dfull = kcfree + 2, *dfree = dfull + 1, *done = dfull + 2, *lbar = done + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lbar + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(lbar + 5);
     float *xd = reinterpret_cast<float *>(sm + oX);
@@ -154,13 +164,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // slots of keys and rows that no copy ever writes, and P, dS, stay or start zero
     for (int e = threadIdx.x; e < oX / 16; e += kThreads) reinterpret_cast<uint4 *>(sm)[e] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2 * kKSlots; i++) mbar_init(&kfull[i], 1);
-        for (int i = 0; i < 2 * kPairs2; i++) mbar_init(&qfull[i], 1);
+        for (int i = 0; i < kKSlots; i++) {
+            mbar_init(&kfull[i], 1);
+            mbar_init(&kfull[kKSlots + i], 1);
+            mbar_init(&kempty[i], 2);
+        }
+        for (int i = 0; i < 3 * kPairs2; i++) mbar_init(&qfull[i], 1);
         mbar_init(sfull, 1);
         mbar_init(pds, 8);
-        mbar_init(drain, 1);
-        for (int i = 0; i < 6; i++) mbar_init(&cfull[i], 1);  // [dq, dk][buffer]
-        for (int i = 0; i < 3; i++) mbar_init(&cfree[i], 4);
+        for (int i = 0; i < 3; i++) mbar_init(&drain[i], 1);
+        mbar_init(qcfull, 1);  // dq's buffer
+        mbar_init(qcfree, 4);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&kcfull[i], 1);  // dk's two
+            mbar_init(&kcfree[i], 4);
+            mbar_init(&done[i], 1);  // the gradients of a tile
+        }
         mbar_init(dfull, 1);
         mbar_init(dfree, 4);
         for (int i = 0; i < 4; i++) mbar_init(&lbar[i], 2);
@@ -177,10 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    uint32_t n_issued = 0;  // the loaders' copies
+    // the loaders' copies; by kind, the slots' next phases and whether a slot was used
+    uint32_t n_issued = 0, n_phase[2] = {0, 0}, n_used[2] = {0, 0};
 
     // Step k: gradients of tile k - 1 and scores of tile k, slice by slice; the
-    // loaders and the issuer walk the same steps.
+    // loaders and the issuers walk the same steps.
     if (warp == kWarpK) {
         // -------------------------------------------------------- keys
         if (lane == 0) {
@@ -188,26 +208,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             Tile cur, prev;
             const uint32_t bytes = (p.W - 1 + kBlock) * 128;
             bool ok = true, hp = false;
-            auto load = [&](const Tile &t, int c) {
+            auto load = [&](const Tile &t, int c, int kind) {
                 const uint32_t s = n_issued % kKSlots;
+                uint64_t *full = &kfull[kind * kKSlots + s];
                 if (n_issued >= kKSlots && !mbar_wait(&kempty[s], (n_issued / kKSlots - 1) & 1, abort_flag, wlim))
                     return false;
                 uint8_t *dst = sm + oK + s * kKSlot;
                 const int x = c < 8 ? 64 * c : 0;
-                mbar_arrive_expect_tx(&kfull[s], bytes);
-                if (p.W > 1) tma_load_3d(dst, c < 8 ? &tm_c : c == 8 ? &tm_h : &tm_l, &kfull[s], x, t.a - (p.W - 1), t.b);
-                tma_load_3d(dst + p.ctxpad * 128, c < 8 ? &tm_c5 : c == 8 ? &tm_h5 : &tm_l5, &kfull[s], x,
+                mbar_arrive_expect_tx(full, bytes);
+                if (p.W > 1) tma_load_3d(dst, c < 8 ? &tm_c : c == 8 ? &tm_h : &tm_l, full, x, t.a - (p.W - 1), t.b);
+                tma_load_3d(dst + p.ctxpad * 128, c < 8 ? &tm_c5 : c == 8 ? &tm_h5 : &tm_l5, full, x,
                             p.S + kBlock * t.n, t.b);
                 n_issued++;
+                n_phase[kind] ^= 1u << s;
+                n_used[kind] |= 1u << s;
                 return true;
             };
             for (;;) {
                 const bool has = cu.next(p, cur);
                 for (int c = 0; ok && c < kSlices; c++) {
-                    if (hp) ok = load(prev, c);
-                    if (ok && has && (!hp || cur.fresh)) ok = load(cur, c);
+                    if (hp) ok = load(prev, c, 0);
+                    if (ok && has && (!hp || cur.fresh)) ok = load(cur, c, 1);
                 }
-                if (ok && has) ok = load(cur, 9);  // the rope keys' lo
+                if (ok && has) ok = load(cur, 9, 1);  // the rope keys' lo
                 if (!ok || !has) break;
                 prev = cur;
                 hp = true;
@@ -220,36 +243,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             Tile cur, prev;
             bool ok = true, hp = false;
             const uint32_t bytes = p.hp * kBlock * 128;
-            auto load = [&](const Tile &t, int c) {
+            auto load = [&](const Tile &t, int c, int kind) {
                 const uint32_t s = n_issued % kPairs2;
+                uint64_t *full = &qfull[kind * kPairs2 + s];
                 if (n_issued >= kPairs2 && !mbar_wait(&qempty[s], (n_issued / kPairs2 - 1) & 1, abort_flag, wlim))
                     return false;
                 uint8_t *dst = sm + oPair + s * kPair;
-                mbar_arrive_expect_tx(&qfull[s], 2 * bytes);
+                mbar_arrive_expect_tx(full, 2 * bytes);
                 if (c < 8) {
-                    tma_load_4d(dst, &tm_q, &qfull[s], 64 * c, kBlock * t.n, t.h0, t.b);
-                    tma_load_4d(dst + kSlot, &tm_g, &qfull[s], 64 * c, kBlock * t.n, t.h0, t.b);
+                    tma_load_4d(dst, &tm_q, full, 64 * c, kBlock * t.n, t.h0, t.b);
+                    tma_load_4d(dst + kSlot, &tm_g, full, 64 * c, kBlock * t.n, t.h0, t.b);
                 } else {
-                    tma_load_4d(dst, &tm_qr, &qfull[s], 0, kBlock * t.n, t.h0, t.b);
-                    tma_load_4d(dst + kSlot, &tm_qr, &qfull[s], 64, kBlock * t.n, t.h0, t.b);
+                    tma_load_4d(dst, &tm_qr, full, 0, kBlock * t.n, t.h0, t.b);
+                    tma_load_4d(dst + kSlot, &tm_qr, full, 64, kBlock * t.n, t.h0, t.b);
                 }
                 n_issued++;
+                n_phase[kind] ^= 1u << s;
+                n_used[kind] |= 1u << s;
                 return true;
             };
             for (;;) {
                 const bool has = cu.next(p, cur);
                 for (int c = 0; ok && c < kSlices; c++) {
-                    if (hp) ok = load(prev, c);
-                    if (ok && has) ok = load(cur, c);
+                    if (hp) ok = load(prev, c, 0);
+                    if (ok && has) ok = load(cur, c, 1);
                 }
                 if (!ok || !has) break;
                 prev = cur;
                 hp = true;
             }
         }
-    } else if (warp == kWarpM) {
+    } else if (warp >= kWarpM) {
         // -------------------------------------------------------- MMAs
+        // Three issuers (one thread of each warp), as a single thread issuing all
+        // products was slower than the products: 0 S and dP, 1 dq, 2 dk and dd.
         if (lane == 0) {
+            const int who = warp - kWarpM;
             const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0), idQ = idesc_bf16(128, 64, 1);
             const uint32_t idK = idesc_bf16_ab(128, 64, 1, 1), idD = idesc_bf16_ab(128, 32, 1, 0);
             const int ksc = p.ctxpad / 16, ksr = (p.hp * kBlock + 15) / 16;
@@ -261,71 +290,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             TileCursor cu(p);
             Tile cur;
             bool ok = true, hp = false;
-            uint32_t kn = 0, qn = 0, i = 0, k = 0;  // slots taken; slices of gradients; steps
+            uint32_t kn = 0, qn = 0, i = 0, k = 0;  // copies of the rings; slices of gradients; steps
             auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
+            // The next copy of a ring, of a kind: its slot, waited for by the issuers
+            // that use it. A parity tells a barrier's phase from the one before only, so
+            // copies for the gradients and for the scores have barriers of their own (an
+            // issuer that skipped a copy on a shared one could pass a phase early).
+            uint32_t kph[2] = {0, 0}, qph[2] = {0, 0};
+            auto take_k = [&](int kind, bool mine) {
+                const uint32_t s = kn++ % kKSlots;
+                if (mine) wait(&kfull[kind * kKSlots + s], (kph[kind] >> s) & 1);
+                kph[kind] ^= 1u << s;
+                return s;
+            };
+            auto take_q = [&](int kind, bool mine) {
+                const uint32_t s = qn++ % kPairs2;
+                if (mine) wait(&qfull[kind * kPairs2 + s], (qph[kind] >> s) & 1);
+                qph[kind] ^= 1u << s;
+                return s;
+            };
             for (; ok; k++) {
                 const bool has = cu.next(p, cur);
                 if (!has && !hp) break;
-                if (hp) {  // P and dS of tile k - 1 are written, its S and dP read
-                    if (!wait(pds, (k - 1) & 1)) break;
-                    tc_fence_after();
-                }
+                // P and dS of tile k - 1 are written, its S and dP read
+                if (hp && !wait(pds, (k - 1) & 1)) break;
+                const bool own = has && (!hp || cur.fresh);  // tile k has keys of its own
+                // slots of keys are released twice: by their two users, or twice by one
+                uint32_t qs1 = 0;
+#pragma unroll 1
                 for (int c = 0; ok && c < kSlices; c++) {
-                    uint32_t ks = 0;
+                    uint32_t ks = 0, qs0 = 0;
                     if (hp) {
-                        ks = kn++ % kKSlots;
-                        const uint32_t qs = qn % kPairs2;
-                        if (!wait(&kfull[ks], ((kn - 1) / kKSlots) & 1) || !wait(&qfull[qs], (qn / kPairs2) & 1)) break;
-                        const SDesc kv = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), kKSlot, 1024));
-                        const SDesc qb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), kSlot, 1024));
-                        const SDesc gb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), kSlot, 1024));
-                        {
-                            const uint32_t n = 2 * i, buf = n % 3, u = n / 3;
-                            if (u > 0 && !wait(&cfree[buf], (u - 1) & 1)) break;
-                            tc_fence_after();
-                            const uint32_t d = tmem + kColC + 64 * buf;
-                            // (unrolled: a product of 64 columns takes 50 cycles, a step of a rolled loop 90)
-#pragma unroll
-                            for (int s = 0; s < 8; s++)
-                                if (s < ksc) mma_bf16_ss(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
-                            mma_bf16_ss(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
-                            mma_commit(&cfull[buf]);
-                        }
-                        {
-                            const uint32_t n = 2 * i + 1, buf = n % 3, u = n / 3;
-                            if (u > 0 && !wait(&cfree[buf], (u - 1) & 1)) break;
-                            tc_fence_after();
-                            const uint32_t d = tmem + kColC + 64 * buf;
-#pragma unroll
-                            for (int s = 0; s < kRows / 16; s++) {
-                                if (s >= ksr) continue;
-                                mma_bf16_ss(d, dst.at(128 * s), qb.at(128 * s), idK, s > 0);
-                                mma_bf16_ss(d, (c < 8 ? pt : dst).at(128 * s), gb.at(128 * s), idK, 1u);
-                            }
-                            mma_commit(&cfull[3 + buf]);
-                        }
-                        if (i > 0 && !wait(dfree, (i - 1) & 1)) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int s = 0; s < kRows / 16; s++)
-                            if (s < ksr) mma_bf16_ss(tmem + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
-                        mma_commit(&qempty[qs]);
-                        if (!has || cur.fresh) mma_commit(&kempty[ks]);
-                        mma_commit(dfull);  // last: nothing is in flight once its reader has it
-                        qn++;
-                        i++;
+                        ks = take_k(0, who == 1 || (who == 0 && has && !own));
+                        qs0 = take_q(0, who == 2);
                     }
                     if (has) {
-                        if (!hp || cur.fresh) {
-                            ks = kn++ % kKSlots;
-                            if (!wait(&kfull[ks], ((kn - 1) / kKSlots) & 1)) break;
+                        if (own) {
+                            const uint32_t s = take_k(1, who == 0);
+                            if (who == 0) ks = s;
                         }
-                        const uint32_t qs = qn % kPairs2;
-                        if (!wait(&qfull[qs], (qn / kPairs2) & 1)) break;
+                        qs1 = take_q(1, who == 0);
+                    }
+                    if (!ok) break;
+                    if (who == 0 && has) {
                         tc_fence_after();
                         const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
-                        const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), 16, 1024));
-                        const SDesc gd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), 16, 1024));
+                        const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs1 * kPair), 16, 1024));
+                        const SDesc gd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs1 * kPair + kSlot), 16, 1024));
                         // the second product: dP; of the rope slice, S again with Q's lo
                         const uint32_t d2 = tmem + (c < 8 ? kColP : kColS);
 #pragma unroll
@@ -333,21 +344,64 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int s = 0; s < 4; s++) mma_bf16_ss(d2, gd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
                         mma_commit(&kempty[ks]);
-                        if (c == 8) {  // Q's hi with the keys' lo
-                            ks = kn++ % kKSlots;
-                            if (!wait(&kfull[ks], ((kn - 1) / kKSlots) & 1)) break;
-                            tc_fence_after();
-                            const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
+                        if (own) mma_commit(&kempty[ks]);
+                        if (c < 8) mma_commit(&qempty[qs1]);
+                    } else if (who == 1 && hp) {
+                        if (i > 0 && !wait(qcfree, (i - 1) & 1)) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + kColC;
+                        const SDesc kv = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), kKSlot, 1024));
+                        // (unrolled: a product of 64 columns takes 50 cycles, a step of a rolled loop 90)
 #pragma unroll
-                            for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), ld.at(2 * s), idS, 1u);
-                            mma_commit(&kempty[ks]);
+                        for (int s = 0; s < 8; s++)
+                            if (s < ksc) mma_bf16_ss(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
+                        mma_bf16_ss(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
+                        mma_commit(&kempty[ks]);
+                        if (!has || own) mma_commit(&kempty[ks]);
+                        if (c == kSlices - 1) mma_commit(&done[0]);
+                        mma_commit(qcfull);  // last: nothing is in flight once its reader has it
+                        i++;
+                    } else if (who == 2 && hp) {
+                        const uint32_t buf = i & 1;
+                        if (i > 1 && !wait(&kcfree[buf], ((i >> 1) - 1) & 1)) break;
+                        tc_fence_after();
+                        const SDesc qb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs0 * kPair), kSlot, 1024));
+                        const SDesc gb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs0 * kPair + kSlot), kSlot, 1024));
+                        const uint32_t d = tmem + kColC + 64 + 64 * buf;
+                        const SDesc p2 = c < 8 ? pt : dst;
+#pragma unroll
+                        for (int s = 0; s < kRows / 16; s++) {
+                            if (s >= ksr) continue;
+                            mma_bf16_ss(d, dst.at(128 * s), qb.at(128 * s), idK, s > 0);
+                            mma_bf16_ss(d, p2.at(128 * s), gb.at(128 * s), idK, 1u);
                         }
-                        mma_commit(&qempty[qs]);
-                        qn++;
+                        mma_commit(&kcfull[buf]);
+                        if (i > 0 && !wait(dfree, (i - 1) & 1)) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int s = 0; s < kRows / 16; s++)
+                            if (s < ksr)
+                                mma_bf16_ss(tmem + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
+                        mma_commit(&qempty[qs0]);
+                        if (c == kSlices - 1) mma_commit(&done[1]);
+                        mma_commit(dfull);  // last
+                        i++;
                     }
                 }
                 if (!ok || !has) break;
-                mma_commit(sfull);
+                const uint32_t ks = take_k(1, who == 0);
+                if (!ok) break;
+                if (who == 0) {  // Q's hi with the keys' lo
+                    tc_fence_after();
+                    const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs1 * kPair), 16, 1024));
+                    const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
+#pragma unroll
+                    for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), ld.at(2 * s), idS, 1u);
+                    mma_commit(&kempty[ks]);
+                    mma_commit(&kempty[ks]);
+                    mma_commit(&qempty[qs1]);
+                    mma_commit(sfull);
+                }
                 hp = true;
             }
         }
@@ -369,17 +423,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float4 *tab = reinterpret_cast<const float4 *>(p.tab + (size_t)(prev.a + j) * (kDR / 2));
 #pragma unroll 1
                 for (int c = 0; c < kSlices; c++, i++) {
-                    const uint32_t buf = 2 * i % 3;
-                    ok = warp_all(mbar_wait(&cfull[buf], (i / 3) & 1, abort_flag, wlim));
+                    ok = warp_all(mbar_wait(qcfull, i & 1, abort_flag, wlim));
                     if (!ok) break;
                     tc_fence_after();
                     float v[2][32];
-                    tmem_ld32(trow + kColC + 64 * buf, v[0]);
-                    tmem_ld32(trow + kColC + 64 * buf + 32, v[1]);
+                    tmem_ld32(trow + kColC, v[0]);
+                    tmem_ld32(trow + kColC + 32, v[1]);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&cfree[buf]);
+                    if (lane == 0) mbar_arrive(qcfree);
                     if (c == 8) {
 #pragma unroll
                         for (int u = 0; u < 16; u++) {
@@ -409,25 +462,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float *base = p.dacc + (size_t)prev.b * p.L * kDK;
 #pragma unroll 1
                 for (int c = 0; c < kSlices; c++, i++) {
-                    const uint32_t buf = (2 * i + 1) % 3;
-                    ok = warp_all(mbar_wait(&cfull[3 + buf], (i / 3) & 1, abort_flag, wlim));
+                    const uint32_t buf = i & 1;
+                    ok = warp_all(mbar_wait(&kcfull[buf], (i >> 1) & 1, abort_flag, wlim));
                     if (!ok) break;
                     tc_fence_after();
                     float v[2][32];
-                    tmem_ld_16x64(trow + kColC + 64 * buf, v[0]);
-                    tmem_ld_16x64(trow + (16u << 16) + kColC + 64 * buf, v[1]);
+                    tmem_ld_16x64(trow + kColC + 64 + 64 * buf, v[0]);
+                    tmem_ld_16x64(trow + (16u << 16) + kColC + 64 + 64 * buf, v[1]);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&cfree[buf]);
+                    if (lane == 0) mbar_arrive(&kcfree[buf]);
+                    // neighbouring lanes trade halves, so that a lane holds four columns of one
+                    // row (even lanes row lane / 4, odd ones 8 rows on) and a quad two full sectors
 #pragma unroll
-                    for (int s = 0; s < 4; s++) {
-                        const int slot = 32 * q4 + 8 * s + (lane >> 2), pos = first + slot;
-                        if (slot < p.W - 1 && pos >= 0) {
-                            float *dst = base + (size_t)pos * kDK + 64 * c + 2 * (lane & 3);
+                    for (int s = 0; s < 2; s++) {
+                        const int slot = 32 * q4 + 16 * s + (lane >> 2) + 8 * (lane & 1), pos = first + slot;
+                        float *dst = base + (size_t)max(pos, 0) * kDK + 64 * c + 2 * (lane & 2);
+                        const bool in = slot < p.W - 1 && pos >= 0;
 #pragma unroll
-                            for (int g = 0; g < 8; g++)
-                                red2(dst + 8 * g, v[s >> 1][4 * g + 2 * (s & 1)], v[s >> 1][4 * g + 2 * (s & 1) + 1]);
+                        for (int g = 0; g < 8; g++) {
+                            float *x = &v[s][4 * g];
+                            const float a0 = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[0] : x[2], 1);
+                            const float a1 = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[1] : x[3], 1);
+                            if (in) {
+                                if (lane & 1) red4(dst + 8 * g, a0, a1, x[2], x[3]);
+                                else red4(dst + 8 * g, x[0], x[1], a0, a1);
+                            }
                         }
                     }
                     // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20);
@@ -454,8 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_all(mbar_wait(sfull, k & 1, abort_flag, wlim));
             if (!ok) break;
             tc_fence_after();
+            // visible context slots of this warp's 64
             const int lo = max(0, p.W - 1 - cur.a) - 64 * hf, hi = (live ? p.W - 1 : -1) - 64 * hf;
-            float P[64], D = 0.f, pd[8], gd[8];
+            const uint32_t in[2] = {slot_mask(lo, hi), slot_mask(lo - 32, hi - 32)};
+            float P[64], D4[4] = {0.f, 0.f, 0.f, 0.f}, pd[8], gd[8];
 #pragma unroll
             for (int x = 0; x < 64; x++) P[x] = 0.f;
             const bool some = 64 * hf < p.ctxpad;  // (ctxpad is a multiple of 32: half a slice may be unused)
@@ -468,11 +531,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(trow + kColP + 64 * hf + 32 * cc, g);
                     tmem_wait_ld();
 #pragma unroll
+                    for (int x = 0; x < 32; x++) s[x] = ex2(fmaf(s[x], p.scale_log2, -z));
+                    if (!warp_all(in[cc] == 0xffffffffu)) {
+#pragma unroll
+                        for (int x = 0; x < 32; x++) {
+                            s[x] = (in[cc] >> x) & 1 ? s[x] : 0.f;
+                            g[x] = (in[cc] >> x) & 1 ? g[x] : 0.f;
+                        }
+                    }
+#pragma unroll
                     for (int x = 0; x < 32; x++) {
-                        const bool in = 32 * cc + x >= lo && 32 * cc + x < hi;
-                        const float e = in ? ex2(fmaf(s[x], p.scale_log2, -z)) : 0.f;
-                        P[32 * cc + x] = e;
-                        D = in ? fmaf(e, g[x], D) : D;
+                        P[32 * cc + x] = s[x];
+                        D4[x & 3] = fmaf(s[x], g[x], D4[x & 3]);
                     }
                 }
             }
@@ -483,15 +553,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < kBlock; x++) {
                     pd[x] = live ? ex2(fmaf(pd[x], p.scale_log2, -z)) : 0.f;
-                    D = live ? fmaf(pd[x], gd[x], D) : 0.f;
+                    D4[0] = live ? fmaf(pd[x], gd[x], D4[0]) : 0.f;
                 }
             }
+            float D = (D4[0] + D4[1]) + (D4[2] + D4[3]);
             xd[hf * 128 + r] = D;
             __syncwarp();
             if (lane == 0) mbar_arrive(&lbar[q4]);
             ok = warp_all(mbar_wait(&lbar[q4], k & 1, abort_flag, wlim));
             if (!ok) break;
             D += xd[(hf ^ 1) * 128 + r];
+            // the products of the tile before have read P and dS
+            if (hp) {
+                ok = warp_all(mbar_wait(&done[0], (k - 1) & 1, abort_flag, wlim)) &&
+                     warp_all(mbar_wait(&done[1], (k - 1) & 1, abort_flag, wlim));
+                if (!ok) break;
+            }
             if (some) {
 #pragma unroll
                 for (int cc = 0; cc < 2; cc++) {
@@ -499,6 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float g[32];
                     tmem_ld32(trow + kColP + 64 * hf + 32 * cc, g);
                     tmem_wait_ld();
+                    if (!warp_all(in[cc] == 0xffffffffu)) {
+#pragma unroll
+                        for (int x = 0; x < 32; x++) g[x] = (in[cc] >> x) & 1 ? g[x] : D;
+                    }
                     if (r < kRows) {
 #pragma unroll
                         for (int u = 0; u < 4; u++) {
@@ -508,10 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const int x = 8 * u + 2 * e;
                                 const float p0 = P[32 * cc + x], p1 = P[32 * cc + x + 1];
                                 a[e] = pack_bf16x2(p0, p1);
-                                const bool i0 = 32 * cc + x >= lo && 32 * cc + x < hi;
-                                const bool i1 = 32 * cc + x + 1 >= lo && 32 * cc + x + 1 < hi;
-                                b[e] = pack_bf16x2(i0 ? p0 * (g[x] - D) * p.scale : 0.f,
-                                                   i1 ? p1 * (g[x + 1] - D) * p.scale : 0.f);
+                                b[e] = pack_bf16x2(p0 * (g[x] - D) * p.scale, p1 * (g[x + 1] - D) * p.scale);
                             }
                             const uint32_t at = hf * kSlot + sw128(r, 4 * cc + u);
                             *reinterpret_cast<uint4 *>(sm + oPr + at) = make_uint4(a[0], a[1], a[2], a[3]);
@@ -545,12 +623,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*abort_flag && lane == 0) {
         volatile int never = 0;
         const uint32_t ring = warp == kWarpK ? kKSlots : kPairs2;
+        uint64_t *full = warp == kWarpK ? kfull : qfull;
         if (warp == kWarpK || warp == kWarpQ)
-            for (uint32_t g = n_issued > ring ? n_issued - ring : 0; g < n_issued; g++)
-                mbar_wait(warp == kWarpK ? &kfull[g % ring] : &qfull[g % ring], (g / ring) & 1, &never);
-        if (warp == kWarpM) {
-            mma_commit(drain);
-            mbar_wait(drain, 0, &never);
+            for (uint32_t s = 0; s < ring; s++)
+                for (int kind = 0; kind < 2; kind++)
+                    if ((n_used[kind] >> s) & 1) mbar_wait(&full[kind * ring + s], ((n_phase[kind] >> s) & 1) ^ 1, &never);
+        if (warp >= kWarpM) {
+            mma_commit(&drain[warp - kWarpM]);
+            mbar_wait(&drain[warp - kWarpM], 0, &never);
         }
     }
     tc_fence_before();

@@ -18,11 +18,11 @@
 // The 132 x 576 fp32 key gradients of a block (304 KB) fit neither tensor
 // memory nor shared memory beside the keys, so a tile's share leaves the SM as
 // it is formed, and keys, Q and dO come in 64-column slices through two rings,
-// twice per tile: for S and dP, and, from L2, for the gradients. The products of
-// the gradients of a tile are interleaved with S and dP of the next, slice by
-// slice, sharing the slice of the keys within a block. What bounds it is this
-// traffic between SMs and L2 (reads 1.1 MB, writes 0.43 MB a tile against 0.36 MB
-// that DRAM has to move).
+// twice per tile: for S and dP, and, from L2, for the gradients. (Gradients of a
+// tile interleaved with S and dP of the next share the keys' slices, but need
+// two slots of Q and dO a slice, and with the three that fit the copies' latency
+// is exposed: 4500 cycles a slice against 2700.) What bounds it is the tensor
+// work, 20000 cycles a tile with its short products, and the reductions.
 //
 // Sums of key gradients are fp32 in whatever order the tiles finish: two runs
 // may differ in the last bits before the rounding to bf16. P and dS are bf16
@@ -46,7 +46,7 @@ using namespace tc;
 
 constexpr int kDL = 512, kDR = 64, kDK = kDL + kDR;
 constexpr int kSlices = 9;
-constexpr int kKeys = 144, kKSlot = kKeys * 128, kKSlots = 4;
+constexpr int kKeys = 144, kKSlot = kKeys * 128, kKSlots = 3;
 constexpr int kHeads = 22, kRows = 112;            // rows of a tile, padded to the K steps of 16
 // Q and dO slices of the same columns; last, hi and lo of Q's rope slice
 constexpr int kSlot = kRows * 128, kPair = 2 * kSlot, kPairs2 = 3;
@@ -54,11 +54,12 @@ constexpr int oK = 0, oPair = kKSlots * kKSlot;
 constexpr int oDS = oPair + kPairs2 * kPair;       // dS, context keys: two slices of 64 keys
 constexpr int oPr = oDS + 2 * kSlot;               // P
 constexpr int oDD = oPr + 2 * kSlot;               // draft keys: [2 x 64 rows][16 dS, 16 P][128 B]
-constexpr int oX = oDD + 2 * 32 * 128;             // D halves [2][128]
+constexpr int oT = oDD + 2 * 32 * 128;             // 4 KB of each reducing warp: 32 rows x 32 columns of dk
+constexpr int oX = oT + 4 * 4096;                  // D halves [2][128]
 constexpr int oBar = oX + 1024;
 constexpr int kSmem = oBar + 512 + 1024;
 static_assert(kHeads * kBlock <= kRows && kSmem <= 232448, "shared memory");
-static_assert(kSlot % 1024 == 0 && oDD % 1024 == 0, "swizzle atoms");
+static_assert(kSlot % 1024 == 0 && oDD % 1024 == 0 && oT % 1024 == 0, "swizzle atoms");
 constexpr uint32_t kColS = 0, kColP = kKeys, kColC = 2 * kKeys, kColD = kColC + 3 * 64;
 constexpr int kWarpK = 8, kWarpQ = 9, kWarpM = 10, kThreads = 13 * 32;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -83,30 +84,12 @@ __device__ __forceinline__ void red4(float *a, float x, float y, float z, float 
 __device__ __forceinline__ void red1(float *a, float x) {
     asm volatile("red.global.add.f32 [%0], %1;" ::"l"(a), "f"(x) : "memory");
 }
-// 16 lanes (from the address's lane) x 64 columns: register 4 g + 2 i + e of
-// lane t is row t / 4 + 8 i, column 8 g + 2 (t % 4) + e.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
-}
-
 // The CTA's tiles in order, over its items: a run of neighbouring blocks, so
 // that CTAs at work at the same time add to different keys (with blocks dealt
 // out in turn, 16 CTAs met on the same keys and the reductions took four times
 // as long).
 struct Tile {
     int b, n, a, h0, nh;
-    bool fresh;  // first of its item: other keys than the tile before
 };
 struct TileCursor {
     DraftCursor cur;
@@ -122,7 +105,6 @@ struct TileCursor {
         w1 = (int)(n * (blockIdx.x + 1) / gridDim.x);
     }
     __device__ __forceinline__ bool next(const Args &p, Tile &o) {
-        o.fresh = !open;
         if (!open) {
             if (w >= w1 || !cur.at(w, it)) return false;
             t = it.t0;
@@ -167,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kKSlots; i++) {
             mbar_init(&kfull[i], 1);
             mbar_init(&kfull[kKSlots + i], 1);
-            mbar_init(&kempty[i], 2);
+            mbar_init(&kempty[i], 1);
         }
         for (int i = 0; i < 3 * kPairs2; i++) mbar_init(&qfull[i], 1);
         mbar_init(sfull, 1);
@@ -199,15 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the loaders' copies; by kind, the slots' next phases and whether a slot was used
     uint32_t n_issued = 0, n_phase[2] = {0, 0}, n_used[2] = {0, 0};
 
-    // Step k: gradients of tile k - 1 and scores of tile k, slice by slice; the
-    // loaders and the issuers walk the same steps.
+    // Per tile the slices for S and dP, then those for the gradients.
     if (warp == kWarpK) {
         // -------------------------------------------------------- keys
         if (lane == 0) {
             TileCursor cu(p);
-            Tile cur, prev;
+            Tile cur;
             const uint32_t bytes = (p.W - 1 + kBlock) * 128;
-            bool ok = true, hp = false;
+            bool ok = true;
             auto load = [&](const Tile &t, int c, int kind) {
                 const uint32_t s = n_issued % kKSlots;
                 uint64_t *full = &kfull[kind * kKSlots + s];
@@ -224,24 +205,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n_used[kind] |= 1u << s;
                 return true;
             };
-            for (;;) {
-                const bool has = cu.next(p, cur);
-                for (int c = 0; ok && c < kSlices; c++) {
-                    if (hp) ok = load(prev, c, 0);
-                    if (ok && has && (!hp || cur.fresh)) ok = load(cur, c, 1);
-                }
-                if (ok && has) ok = load(cur, 9, 1);  // the rope keys' lo
-                if (!ok || !has) break;
-                prev = cur;
-                hp = true;
+            while (ok && cu.next(p, cur)) {
+                for (int c = 0; ok && c <= kSlices; c++) ok = load(cur, c, 1);  // (9: the rope keys' lo)
+                for (int c = 0; ok && c < kSlices; c++) ok = load(cur, c, 0);
             }
         }
     } else if (warp == kWarpQ) {
         // ---------------------------------------------------- Q and dO
         if (lane == 0) {
             TileCursor cu(p);
-            Tile cur, prev;
-            bool ok = true, hp = false;
+            Tile cur;
+            bool ok = true;
             const uint32_t bytes = p.hp * kBlock * 128;
             auto load = [&](const Tile &t, int c, int kind) {
                 const uint32_t s = n_issued % kPairs2;
@@ -262,16 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n_used[kind] |= 1u << s;
                 return true;
             };
-            for (;;) {
-                const bool has = cu.next(p, cur);
-                for (int c = 0; ok && c < kSlices; c++) {
-                    if (hp) ok = load(prev, c, 0);
-                    if (ok && has) ok = load(cur, c, 1);
-                }
-                if (!ok || !has) break;
-                prev = cur;
-                hp = true;
-            }
+            while (ok && cu.next(p, cur))
+                for (int kind = 1; kind >= 0; kind--)
+                    for (int c = 0; ok && c < kSlices; c++) ok = load(cur, c, kind);
         }
     } else if (warp >= kWarpM) {
         // -------------------------------------------------------- MMAs
@@ -289,54 +256,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             const SDesc ddb = sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 16, 1024));         // draft keys x rows
             TileCursor cu(p);
             Tile cur;
-            bool ok = true, hp = false;
-            uint32_t kn = 0, qn = 0, i = 0, k = 0;  // copies of the rings; slices of gradients; steps
+            bool ok = true;
+            uint32_t i = 0, k = 0;  // slices of gradients; tiles
             auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
-            // The next copy of a ring, of a kind: its slot, waited for by the issuers
-            // that use it. A parity tells a barrier's phase from the one before only, so
-            // copies for the gradients and for the scores have barriers of their own (an
-            // issuer that skipped a copy on a shared one could pass a phase early).
-            uint32_t kph[2] = {0, 0}, qph[2] = {0, 0};
-            auto take_k = [&](int kind, bool mine) {
-                const uint32_t s = kn++ % kKSlots;
-                if (mine) wait(&kfull[kind * kKSlots + s], (kph[kind] >> s) & 1);
-                kph[kind] ^= 1u << s;
+            // Copy n of a ring, of a kind: its slot, once it has landed. A parity tells a
+            // barrier's phase from the one before only, so copies for the scores and for
+            // the gradients, which have other users, have barriers of their own (a user
+            // that skipped a copy on a shared one could pass a phase early).
+            uint32_t kph = 0, qph = 0;
+            auto take_k = [&](int kind, uint32_t n) {
+                const uint32_t s = n % kKSlots;
+                wait(&kfull[kind * kKSlots + s], (kph >> s) & 1);
+                kph ^= 1u << s;
                 return s;
             };
-            auto take_q = [&](int kind, bool mine) {
-                const uint32_t s = qn++ % kPairs2;
-                if (mine) wait(&qfull[kind * kPairs2 + s], (qph[kind] >> s) & 1);
-                qph[kind] ^= 1u << s;
+            auto take_q = [&](int kind, uint32_t n) {
+                const uint32_t s = n % kPairs2;
+                wait(&qfull[kind * kPairs2 + s], (qph >> s) & 1);
+                qph ^= 1u << s;
                 return s;
             };
-            for (; ok; k++) {
-                const bool has = cu.next(p, cur);
-                if (!has && !hp) break;
-                // P and dS of tile k - 1 are written, its S and dP read
-                if (hp && !wait(pds, (k - 1) & 1)) break;
-                const bool own = has && (!hp || cur.fresh);  // tile k has keys of its own
-                // slots of keys are released twice: by their two users, or twice by one
-                uint32_t qs1 = 0;
+            for (; ok && cu.next(p, cur); k++) {
+                const uint32_t kn = k * (2 * kSlices + 1), qn = k * 2 * kSlices;  // the tile's first copies
+                if (who == 0) {
+                    // S and dP of the tile before are read
+                    if (k > 0 && !wait(pds, (k - 1) & 1)) break;
 #pragma unroll 1
-                for (int c = 0; ok && c < kSlices; c++) {
-                    uint32_t ks = 0, qs0 = 0;
-                    if (hp) {
-                        ks = take_k(0, who == 1 || (who == 0 && has && !own));
-                        qs0 = take_q(0, who == 2);
-                    }
-                    if (has) {
-                        if (own) {
-                            const uint32_t s = take_k(1, who == 0);
-                            if (who == 0) ks = s;
-                        }
-                        qs1 = take_q(1, who == 0);
-                    }
-                    if (!ok) break;
-                    if (who == 0 && has) {
+                    for (int c = 0; c < kSlices; c++) {
+                        const uint32_t ks = take_k(1, kn + c), qs = take_q(1, qn + c);
+                        if (!ok) break;
                         tc_fence_after();
                         const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
-                        const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs1 * kPair), 16, 1024));
-                        const SDesc gd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs1 * kPair + kSlot), 16, 1024));
+                        const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), 16, 1024));
+                        const SDesc gd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), 16, 1024));
                         // the second product: dP; of the rope slice, S again with Q's lo
                         const uint32_t d2 = tmem + (c < 8 ? kColP : kColS);
 #pragma unroll
@@ -344,10 +296,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int s = 0; s < 4; s++) mma_bf16_ss(d2, gd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
                         mma_commit(&kempty[ks]);
-                        if (own) mma_commit(&kempty[ks]);
-                        if (c < 8) mma_commit(&qempty[qs1]);
-                    } else if (who == 1 && hp) {
-                        if (i > 0 && !wait(qcfree, (i - 1) & 1)) break;
+                        if (c == kSlices - 1) {  // Q's hi with the keys' lo
+                            const uint32_t kl = take_k(1, kn + kSlices);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + oK + kl * kKSlot), 16, 1024));
+#pragma unroll
+                            for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), ld.at(2 * s), idS, 1u);
+                            mma_commit(&kempty[kl]);
+                        }
+                        mma_commit(&qempty[qs]);
+                    }
+                    if (ok) mma_commit(sfull);
+                    continue;
+                }
+                if (!wait(pds, k & 1)) break;  // P and dS are written
+#pragma unroll 1
+                for (int c = 0; c < kSlices; c++, i++) {
+                    if (who == 1) {
+                        const uint32_t ks = take_k(0, kn + kSlices + 1 + c);
+                        if (!ok || (i > 0 && !wait(qcfree, (i - 1) & 1))) break;
                         tc_fence_after();
                         const uint32_t d = tmem + kColC;
                         const SDesc kv = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), kKSlot, 1024));
@@ -357,16 +325,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (s < ksc) mma_bf16_ss(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
                         mma_bf16_ss(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
                         mma_commit(&kempty[ks]);
-                        if (!has || own) mma_commit(&kempty[ks]);
                         if (c == kSlices - 1) mma_commit(&done[0]);
                         mma_commit(qcfull);  // last: nothing is in flight once its reader has it
-                        i++;
-                    } else if (who == 2 && hp) {
-                        const uint32_t buf = i & 1;
-                        if (i > 1 && !wait(&kcfree[buf], ((i >> 1) - 1) & 1)) break;
+                    } else {
+                        const uint32_t qs = take_q(0, qn + kSlices + c), buf = i & 1;
+                        if (!ok || (i > 1 && !wait(&kcfree[buf], ((i >> 1) - 1) & 1))) break;
                         tc_fence_after();
-                        const SDesc qb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs0 * kPair), kSlot, 1024));
-                        const SDesc gb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs0 * kPair + kSlot), kSlot, 1024));
+                        const SDesc qb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), kSlot, 1024));
+                        const SDesc gb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), kSlot, 1024));
                         const uint32_t d = tmem + kColC + 64 + 64 * buf;
                         const SDesc p2 = c < 8 ? pt : dst;
 #pragma unroll
@@ -382,27 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int s = 0; s < kRows / 16; s++)
                             if (s < ksr)
                                 mma_bf16_ss(tmem + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
-                        mma_commit(&qempty[qs0]);
+                        mma_commit(&qempty[qs]);
                         if (c == kSlices - 1) mma_commit(&done[1]);
                         mma_commit(dfull);  // last
-                        i++;
                     }
                 }
-                if (!ok || !has) break;
-                const uint32_t ks = take_k(1, who == 0);
-                if (!ok) break;
-                if (who == 0) {  // Q's hi with the keys' lo
-                    tc_fence_after();
-                    const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs1 * kPair), 16, 1024));
-                    const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
-#pragma unroll
-                    for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), ld.at(2 * s), idS, 1u);
-                    mma_commit(&kempty[ks]);
-                    mma_commit(&kempty[ks]);
-                    mma_commit(&qempty[qs1]);
-                    mma_commit(sfull);
-                }
-                hp = true;
             }
         }
     } else if (warp < 8) {
@@ -410,105 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q4 = warp & 3, hf = warp >> 2, r = q4 * 32 + lane, j = r % kBlock, hl = r / kBlock;
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
         TileCursor cu(p);
-        Tile cur, prev;
-        bool ok = true, hp = false;
+        Tile cur;
+        bool ok = true;
         uint32_t i = 0, k = 0;
-        for (; ok; k++) {
-            const bool has = cu.next(p, cur);
-            if (hp && hf == 0) {
-                // dq of tile k - 1: the rope slice turned back
-                const bool live = hl < prev.nh;
-                const size_t row = ((size_t)prev.b * p.n_h + prev.h0 + (live ? hl : 0)) * p.R + (size_t)kBlock * prev.n + j;
-                uint8_t *dst = reinterpret_cast<uint8_t *>(p.dq + row * kDK);
-                const float4 *tab = reinterpret_cast<const float4 *>(p.tab + (size_t)(prev.a + j) * (kDR / 2));
-#pragma unroll 1
-                for (int c = 0; c < kSlices; c++, i++) {
-                    ok = warp_all(mbar_wait(qcfull, i & 1, abort_flag, wlim));
-                    if (!ok) break;
-                    tc_fence_after();
-                    float v[2][32];
-                    tmem_ld32(trow + kColC, v[0]);
-                    tmem_ld32(trow + kColC + 32, v[1]);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(qcfree);
-                    if (c == 8) {
-#pragma unroll
-                        for (int u = 0; u < 16; u++) {
-                            const float4 cs = __ldg(tab + u);
-                            float *x = &v[u >> 3][4 * (u & 7)];
-                            const float x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
-                            x[0] = x0 * cs.x + x1 * cs.y;
-                            x[1] = x1 * cs.x - x0 * cs.y;
-                            x[2] = x2 * cs.z + x3 * cs.w;
-                            x[3] = x3 * cs.z - x2 * cs.w;
-                        }
-                    }
-                    if (live) {
-#pragma unroll
-                        for (int u = 0; u < 4; u++) {
-                            uint32_t x[8];
-#pragma unroll
-                            for (int e = 0; e < 8; e++)
-                                x[e] = pack_bf16x2(v[u >> 1][16 * (u & 1) + 2 * e], v[u >> 1][16 * (u & 1) + 2 * e + 1]);
-                            st_global_32B(dst + 128 * c + 32 * u, x, p.wide);
-                        }
-                    }
-                }
-            } else if (hp) {
-                // dk: key slots 32 q4 + 16 s + lane / 4 (+ 8), eight columns to a quad
-                const int first = prev.a - (p.W - 1);
-                float *base = p.dacc + (size_t)prev.b * p.L * kDK;
-#pragma unroll 1
-                for (int c = 0; c < kSlices; c++, i++) {
-                    const uint32_t buf = i & 1;
-                    ok = warp_all(mbar_wait(&kcfull[buf], (i >> 1) & 1, abort_flag, wlim));
-                    if (!ok) break;
-                    tc_fence_after();
-                    float v[2][32];
-                    tmem_ld_16x64(trow + kColC + 64 + 64 * buf, v[0]);
-                    tmem_ld_16x64(trow + (16u << 16) + kColC + 64 + 64 * buf, v[1]);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&kcfree[buf]);
-                    // neighbouring lanes trade halves, so that a lane holds four columns of one
-                    // row (even lanes row lane / 4, odd ones 8 rows on) and a quad two full sectors
-#pragma unroll
-                    for (int s = 0; s < 2; s++) {
-                        const int slot = 32 * q4 + 16 * s + (lane >> 2) + 8 * (lane & 1), pos = first + slot;
-                        float *dst = base + (size_t)max(pos, 0) * kDK + 64 * c + 2 * (lane & 2);
-                        const bool in = slot < p.W - 1 && pos >= 0;
-#pragma unroll
-                        for (int g = 0; g < 8; g++) {
-                            float *x = &v[s][4 * g];
-                            const float a0 = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[0] : x[2], 1);
-                            const float a1 = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[1] : x[3], 1);
-                            if (in) {
-                                if (lane & 1) red4(dst + 8 * g, a0, a1, x[2], x[3]);
-                                else red4(dst + 8 * g, x[0], x[1], a0, a1);
-                            }
-                        }
-                    }
-                    // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20);
-                    // of the rope slice, lanes 64 - 127 its lo's share of dS_d
-                    ok = warp_all(mbar_wait(dfull, i & 1, abort_flag, wlim));
-                    if (!ok) break;
-                    tc_fence_after();
-                    float d[8];
-                    tmem_ld8(trow + kColD + (q4 >= 2 && c < 8 ? 16 : 0), d);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(dfree);
-                    float *dst = base + (size_t)(p.S + kBlock * prev.n) * kDK + 64 * c + (r & 63);
-#pragma unroll
-                    for (int e = 0; e < kBlock; e++) red1(dst + (size_t)e * kDK, d[e]);
-                }
-            }
-            if (!ok || !has) break;
-            // softmax of tile k: this warp's 64 context keys, warps 0 - 3 the draft keys too
+        for (; ok && cu.next(p, cur); k++) {
+            // softmax: this warp's 64 context keys, warps 0 - 3 the draft keys too
             const bool live = hl < cur.nh;
             const float z = live ? p.lse[((size_t)cur.b * p.n_h + cur.h0 + hl) * p.R + (size_t)kBlock * cur.n + j] * kLog2e
                                  : 0.f;
@@ -564,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             D += xd[(hf ^ 1) * 128 + r];
             // the products of the tile before have read P and dS
-            if (hp) {
+            if (k > 0) {
                 ok = warp_all(mbar_wait(&done[0], (k - 1) & 1, abort_flag, wlim)) &&
                      warp_all(mbar_wait(&done[1], (k - 1) & 1, abort_flag, wlim));
                 if (!ok) break;
@@ -613,8 +469,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(pds);
-            prev = cur;
-            hp = true;
+            if (hf == 0) {
+                // dq: the rope slice turned back
+                const bool live = hl < cur.nh;
+                const size_t row = ((size_t)cur.b * p.n_h + cur.h0 + (live ? hl : 0)) * p.R + (size_t)kBlock * cur.n + j;
+                uint8_t *dst = reinterpret_cast<uint8_t *>(p.dq + row * kDK);
+                const float4 *tab = reinterpret_cast<const float4 *>(p.tab + (size_t)(cur.a + j) * (kDR / 2));
+#pragma unroll 1
+                for (int c = 0; c < kSlices; c++, i++) {
+                    ok = warp_all(mbar_wait(qcfull, i & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float v[2][32];
+                    tmem_ld32(trow + kColC, v[0]);
+                    tmem_ld32(trow + kColC + 32, v[1]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(qcfree);
+                    if (c == 8) {
+#pragma unroll
+                        for (int u = 0; u < 16; u++) {
+                            const float4 cs = __ldg(tab + u);
+                            float *x = &v[u >> 3][4 * (u & 7)];
+                            const float x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
+                            x[0] = x0 * cs.x + x1 * cs.y;
+                            x[1] = x1 * cs.x - x0 * cs.y;
+                            x[2] = x2 * cs.z + x3 * cs.w;
+                            x[3] = x3 * cs.z - x2 * cs.w;
+                        }
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                x[e] = pack_bf16x2(v[u >> 1][16 * (u & 1) + 2 * e], v[u >> 1][16 * (u & 1) + 2 * e + 1]);
+                            st_global_32B(dst + 128 * c + 32 * u, x, p.wide);
+                        }
+                    }
+                }
+            } else {
+                // dk: the warp's 32 key slots, 32 columns at a time through shared memory, so
+                // that a reduction adds whole 128-byte lines of four rows (rows one to a
+                // lane, 16 or 32 bytes of a line each, took 2.5 times as long)
+                const int first = cur.a - (p.W - 1);
+                float *base = p.dacc + (size_t)cur.b * p.L * kDK;
+                uint8_t *stg = sm + oT + q4 * 4096;
+#pragma unroll 1
+                for (int c = 0; c < kSlices; c++, i++) {
+                    const uint32_t buf = i & 1;
+                    ok = warp_all(mbar_wait(&kcfull[buf], (i >> 1) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float v[2][32];
+                    tmem_ld32(trow + kColC + 64 + 64 * buf, v[0]);
+                    tmem_ld32(trow + kColC + 64 + 64 * buf + 32, v[1]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kcfree[buf]);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < 8; u++)
+                            *reinterpret_cast<float4 *>(stg + sw128(lane, u)) =
+                                make_float4(v[h][4 * u], v[h][4 * u + 1], v[h][4 * u + 2], v[h][4 * u + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < 8; u++) {
+                            const int row = 4 * u + (lane >> 3), slot = 32 * q4 + row, pos = first + slot;
+                            const float4 x = *reinterpret_cast<const float4 *>(stg + sw128(row, lane & 7));
+                            if (slot < p.W - 1 && pos >= 0)
+                                red4(base + (size_t)pos * kDK + 64 * c + 32 * h + 4 * (lane & 7), x.x, x.y, x.z, x.w);
+                        }
+                    }
+                    // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20);
+                    // of the rope slice, lanes 64 - 127 its lo's share of dS_d
+                    ok = warp_all(mbar_wait(dfull, i & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float d[8];
+                    tmem_ld8(trow + kColD + (q4 >= 2 && c < 8 ? 16 : 0), d);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dfree);
+                    float *dst = base + (size_t)(p.S + kBlock * cur.n) * kDK + 64 * c + (r & 63);
+#pragma unroll
+                    for (int e = 0; e < kBlock; e++) red1(dst + (size_t)e * kDK, d[e]);
+                }
+            }
         }
     }
 

@@ -32,8 +32,8 @@
 //
 // TMEM: S 0..143, dP 144..287, dq 288..351, dk 352..415 / 416..479, dd 480..511.
 // Warps 0-7 softmax (warps w and w + 4 share 32 rows, 64 context keys each);
-// 0-3 then store dq, 4-7 reduce dk and dd; 8 loads keys, 9 Q and dO, 10 - 12
-// issue the MMAs. Every wait is bounded.
+// 0-3 then take dq and dd, 4-7 dk; 8 loads keys, 9 Q and dO, 10 - 12 issue the
+// MMAs, 13 stores dq. Every wait is bounded.
 #include <algorithm>
 
 #include "dspark_latent_tc.cuh"
@@ -46,7 +46,7 @@ using namespace tc;
 
 constexpr int kDL = 512, kDR = 64, kDK = kDL + kDR;
 constexpr int kSlices = 9;
-constexpr int kKeys = 144, kKSlot = kKeys * 128, kKSlots = 3;
+constexpr int kKeys = 144, kKSlot = kKeys * 128, kKSlots = 2;
 constexpr int kHeads = 22, kRows = 112;            // rows of a tile, padded to the K steps of 16
 // Q and dO slices of the same columns; last, hi and lo of Q's rope slice
 constexpr int kSlot = kRows * 128, kPair = 2 * kSlot, kPairs2 = 3;
@@ -55,13 +55,14 @@ constexpr int oDS = oPair + kPairs2 * kPair;       // dS, context keys: two slic
 constexpr int oPr = oDS + 2 * kSlot;               // P
 constexpr int oDD = oPr + 2 * kSlot;               // draft keys: [2 x 64 rows][16 dS, 16 P][128 B]
 constexpr int oT = oDD + 2 * 32 * 128;             // 4 KB of each reducing warp: 32 rows x 32 columns of dk
-constexpr int oX = oT + 4 * 4096;                  // D halves [2][128]
+constexpr int oO = oT + 4 * 4096;                  // dq on its way out: rows x 64 columns
+constexpr int oX = oO + kSlot;                     // D halves [2][128]
 constexpr int oBar = oX + 1024;
 constexpr int kSmem = oBar + 512 + 1024;
 static_assert(kHeads * kBlock <= kRows && kSmem <= 232448, "shared memory");
 static_assert(kSlot % 1024 == 0 && oDD % 1024 == 0 && oT % 1024 == 0, "swizzle atoms");
 constexpr uint32_t kColS = 0, kColP = kKeys, kColC = 2 * kKeys, kColD = kColC + 3 * 64;
-constexpr int kWarpK = 8, kWarpQ = 9, kWarpM = 10, kThreads = 13 * 32;
+constexpr int kWarpK = 8, kWarpQ = 9, kWarpM = 10, kWarpO = 13, kThreads = 14 * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -71,11 +72,9 @@ struct Args {
     const int32_t *cnt, *sorted_n, *sorted_a;
     const float2 *tab;
     const float *lse;
-    __nv_bfloat16 *dq;
     float *dacc;
     uint32_t *err;
     uint64_t wait_ns;
-    bool wide;
 };
 
 __device__ __forceinline__ void red4(float *a, float x, float y, float z, float w) {
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_c,
                  const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_l,
                  const __grid_constant__ CUtensorMap tm_c5, const __grid_constant__ CUtensorMap tm_h5,
-                 const __grid_constant__ CUtensorMap tm_l5, const Args p) {
+                 const __grid_constant__ CUtensorMap tm_l5, const __grid_constant__ CUtensorMap tm_dq, const Args p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     // a slot's full barriers: [0] of copies for the gradients, [1] of those for the scores
@@ -136,9 +135,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *qfull = kempty + kKSlots, *qempty = qfull + 2 * kPairs2;
     uint64_t *sfull = qempty + kPairs2, *pds = sfull + 1, *drain = sfull + 2;
     uint64_t *qcfull = sfull + 5, *qcfree = qcfull + 1, *kcfull = qcfull + 2, *kcfree = kcfull + 2;
-    uint64_t *dfull = kcfree + 2, *dfree = dfull + 1, *done = dfull + 2, *lbar = done + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lbar + 4);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(lbar + 5);
+    uint64_t *dfull = kcfree + 2, *dfree = dfull + 1, *done = dfull + 2, *lbar = done + 2, *ofull = lbar + 4, *ofree = ofull + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ofree + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(ofree + 2);
     float *xd = reinterpret_cast<float *>(sm + oX);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t wlim = p.wait_ns;
@@ -162,6 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&kcfree[i], 4);
             mbar_init(&done[i], 1);  // the gradients of a tile
         }
+        mbar_init(ofull, 4);
+        mbar_init(ofree, 1);
         mbar_init(dfull, 1);
         mbar_init(dfree, 4);
         for (int i = 0; i < 4; i++) mbar_init(&lbar[i], 2);
@@ -239,6 +240,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && cu.next(p, cur))
                 for (int kind = 1; kind >= 0; kind--)
                     for (int c = 0; ok && c < kSlices; c++) ok = load(cur, c, kind);
+        }
+    } else if (warp == kWarpO) {
+        // ---------------------------------------------------- dq -> memory
+        if (lane == 0) {
+            TileCursor cu(p);
+            Tile cur;
+            uint32_t i = 0;
+            bool ok = true;
+            while (ok && cu.next(p, cur))
+                for (int c = 0; c < kSlices; c++, i++) {
+                    if (!(ok = mbar_wait(ofull, i & 1, abort_flag, wlim))) break;
+                    tma_store_4d(&tm_dq, sm + oO, 64 * c, kBlock * cur.n, cur.h0, cur.b);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                    mbar_arrive(ofree);
+                }
+            bulk_wait_all();
         }
     } else if (warp >= kWarpM) {
         // -------------------------------------------------------- MMAs
@@ -471,10 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(pds);
             if (hf == 0) {
                 // dq: the rope slice turned back
-                const bool live = hl < cur.nh;
-                const size_t row = ((size_t)cur.b * p.n_h + cur.h0 + (live ? hl : 0)) * p.R + (size_t)kBlock * cur.n + j;
-                uint8_t *dst = reinterpret_cast<uint8_t *>(p.dq + row * kDK);
                 const float4 *tab = reinterpret_cast<const float4 *>(p.tab + (size_t)(cur.a + j) * (kDR / 2));
+                float *dd = p.dacc + ((size_t)cur.b * p.L + p.S + kBlock * cur.n) * kDK + (r & 63);
 #pragma unroll 1
                 for (int c = 0; c < kSlices; c++, i++) {
                     ok = warp_all(mbar_wait(qcfull, i & 1, abort_flag, wlim));
@@ -499,16 +515,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x[3] = x3 * cs.z - x2 * cs.w;
                         }
                     }
-                    if (live) {
+                    if (i > 0) ok = warp_all(mbar_wait(ofree, (i - 1) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    if (r < kRows) {
 #pragma unroll
-                        for (int u = 0; u < 4; u++) {
-                            uint32_t x[8];
-#pragma unroll
-                            for (int e = 0; e < 8; e++)
-                                x[e] = pack_bf16x2(v[u >> 1][16 * (u & 1) + 2 * e], v[u >> 1][16 * (u & 1) + 2 * e + 1]);
-                            st_global_32B(dst + 128 * c + 32 * u, x, p.wide);
+                        for (int u = 0; u < 8; u++) {
+                            const float *x = &v[u >> 2][8 * (u & 3)];
+                            *reinterpret_cast<uint4 *>(sm + oO + sw128(r, u)) =
+                                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                           pack_bf16x2(x[6], x[7]));
                         }
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ofull);
+                    // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20);
+                    // of the rope slice, lanes 64 - 127 its lo's share of dS_d
+                    ok = warp_all(mbar_wait(dfull, i & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float d[8];
+                    tmem_ld8(trow + kColD + (q4 >= 2 && c < 8 ? 16 : 0), d);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dfree);
+#pragma unroll
+                    for (int e = 0; e < kBlock; e++) red1(dd + (size_t)e * kDK + 64 * c, d[e]);
                 }
             } else {
                 // dk: the warp's 32 key slots, 32 columns at a time through shared memory, so
@@ -546,20 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 red4(base + (size_t)pos * kDK + 64 * c + 32 * h + 4 * (lane & 7), x.x, x.y, x.z, x.w);
                         }
                     }
-                    // dd: lanes 0 - 63 Q^T dS_d (columns 0 - 4), lanes 64 - 127 dO^T P_d (columns 16 - 20);
-                    // of the rope slice, lanes 64 - 127 its lo's share of dS_d
-                    ok = warp_all(mbar_wait(dfull, i & 1, abort_flag, wlim));
-                    if (!ok) break;
-                    tc_fence_after();
-                    float d[8];
-                    tmem_ld8(trow + kColD + (q4 >= 2 && c < 8 ? 16 : 0), d);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(dfree);
-                    float *dst = base + (size_t)(p.S + kBlock * cur.n) * kDK + 64 * c + (r & 63);
-#pragma unroll
-                    for (int e = 0; e < kBlock; e++) red1(dst + (size_t)e * kDK, d[e]);
                 }
             }
         }
@@ -575,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t s = 0; s < ring; s++)
                 for (int kind = 0; kind < 2; kind++)
                     if ((n_used[kind] >> s) & 1) mbar_wait(&full[kind * ring + s], ((n_phase[kind] >> s) & 1) ^ 1, &never);
-        if (warp >= kWarpM) {
+        if (warp >= kWarpM && warp < kWarpO) {
             mma_commit(&drain[warp - kWarpM]);
             mbar_wait(&drain[warp - kWarpM], 0, &never);
         }
@@ -687,12 +706,10 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
         a.sorted_a = ws.base.sorted_a;
         a.tab = ws.base.rope;
         a.lse = lse;
-        a.dq = (__nv_bfloat16 *)dq;
         a.dacc = ws.dacc;
         a.err = ws.base.err;
         a.wait_ns = p.wait_ns;
-        a.wide = ((uintptr_t)dq & 31) == 0;
-        CUtensorMap mq, mg, mr, mc, mh, ml, mc5, mh5, ml5;
+        CUtensorMap mq, mg, mr, mc, mh, ml, mc5, mh5, ml5, mdq;
         const uint64_t L = p.L, B = p.B, R = p.R, H = p.n_h;
         const uint64_t qd[4] = {kDK, R, H, B}, qs[3] = {kDK * 2, R * kDK * 2, H * R * kDK * 2};
         const uint64_t gd[4] = {kDL, R, H, B}, gs[3] = {kDL * 2, R * kDL * 2, H * R * kDL * 2};
@@ -701,7 +718,7 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
         const uint64_t cd[3] = {kDL, L, B}, cs[2] = {kDL * 2, L * kDL * 2};
         const uint64_t rd[3] = {kDR, L, B}, rs[2] = {kDR * 2, L * kDR * 2};
         const uint32_t wb[3] = {64, (uint32_t)std::max(p.W - 1, 1), 1}, db[3] = {64, kBlock, 1};
-        if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mg, dout, 4, gd, gs, qb) ||
+        if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mdq, dq, 4, qd, qs, qb) || !make_map_nd(&mg, dout, 4, gd, gs, qb) ||
             !make_map_nd(&mr, ws.q_rot, 4, sd, ss, qb) || !make_map_nd(&mc, c, 3, cd, cs, wb) ||
             !make_map_nd(&mh, ws.kr_hi, 3, rd, rs, wb) || !make_map_nd(&mc5, c, 3, cd, cs, db) ||
             !make_map_nd(&mh5, ws.kr_hi, 3, rd, rs, db) || !make_map_nd(&ml, ws.kr_lo, 3, rd, rs, wb) ||
@@ -711,7 +728,7 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
         if (e != cudaSuccess) return e;
         count_launch();
         e = launch_pdl(k_lat_bwd_tc, dim3(std::min(a.n_work, nsm)), dim3(kThreads), kSmem, st, mq, mg, mr, mc, mh, ml,
-                       mc5, mh5, ml5, a);
+                       mc5, mh5, ml5, mdq, a);
         if (e != cudaSuccess) return e;
     }
     count_launch();

@@ -35,6 +35,15 @@ __device__ __forceinline__ uint32_t slot_mask(int lo, int hi) {
     if (hi <= 0 || lo >= 32 || hi <= lo) return 0u;
     return (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & ~(lo <= 0 ? 0u : (1u << lo) - 1u);
 }
+// 4-D tiled TMA store and this thread's bulk group.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *m, const void *src, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"((uint64_t)m),
+                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // 32 bytes to global memory: one store where the address allows it.
 __device__ __forceinline__ void st_global_32B(void *p, const uint32_t (&v)[8], bool wide) {
     if (wide) {

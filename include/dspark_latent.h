@@ -145,7 +145,8 @@ DSPARK_API dspark_status dspark_latent_cache_read(const dspark_latent_cache *p, 
  * q_start, nothing), and dspark_get_error returns DSPARK_ERR_PAGE.
  * kind F32 goes with dtype F32, BF16 and FP8 with dtype BF16.
  * Limits: n_h >= 1, n_seq >= 0, T >= 0, page_size >= 1, widths as the cache,
- *   T * n_h < 2^31, max_pages * page_size < 2^31, window >= 0.
+ *   T * n_h < 2^31, max_pages * page_size < 2^31, n_pages * page_size < 2^31,
+ *   n_seq < 2^24, window >= 0.
  * max_kv_len, a bound of kv_len known to the caller, only sets how the keys are
  * split over the GPU (0 = max_pages * page_size). */
 typedef struct {

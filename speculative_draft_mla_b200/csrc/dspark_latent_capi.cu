@@ -112,7 +112,8 @@ dspark_status make_paged(const dspark_latent_paged *pp, Paged *out) {
         return DSPARK_ERR_SHAPE;
     if (!good_widths(p.kind, p.d_l, p.d_r)) return DSPARK_ERR_UNSUPPORTED;
     const long long lim = 1ll << 31;
-    if ((long long)p.T * p.n_h >= lim || (long long)p.max_pages * p.page_size >= lim || p.n_seq >= (1 << 24))
+    if ((long long)p.T * p.n_h >= lim || (long long)p.max_pages * p.page_size >= lim || p.n_seq >= (1 << 24) ||
+        (long long)p.n_pages * p.page_size >= lim)
         return DSPARK_ERR_UNSUPPORTED;
     Paged r{};
     r.n_seq = p.n_seq; r.T = p.T; r.n_h = p.n_h; r.d_l = p.d_l; r.d_r = p.d_r;

@@ -39,9 +39,10 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         return;
     }
     __shared__ long long wsteps[32], carry_steps;
-    __shared__ int wtiles[32], carry_tiles, bad;
+    __shared__ int wtiles[32], carry_tiles, bad, n_split;
     if (threadIdx.x == 0) {
         bad = 0;
+        n_split = 0;
         carry_steps = 0;
         carry_tiles = 0;
     }
@@ -120,7 +121,10 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
             for (int r = threadIdx.x; r < n; r += blockDim.x) {
                 const long long a = w.start[r], b = w.start[r + 1];
                 for (long long i = (a + X - 1) / X; i < kPairs && i * X < b; i++) w.first[i] = r;
+                if (a / X != (b - 1) / X) w.split[atomicAdd(&n_split, 1)] = r;  // (at most one for each end of a pair)
             }
+        __syncthreads();
+        if (threadIdx.x == 0) w.head->n_split = n_split;
     }
     if (threadIdx.x == 0) *p.err = bad ? kErrPage : 0u;
 }
@@ -146,6 +150,7 @@ size_t paged_layout(const Paged &p, void *ws, PagedPlan *w) {
         return (void *)at;
     };
     r.first = (int *)take(sizeof(int) * kPairs);
+    r.split = (int *)take(sizeof(int) * kPairs);
     r.tiles = (int4 *)take(sizeof(int4) * ((size_t)r.max_tiles + 1));
     r.start = (long long *)take(sizeof(long long) * ((size_t)r.max_tiles + 1));
     r.tab = (float2 *)take(sizeof(float2) * 32 * (size_t)p.T);
@@ -162,7 +167,7 @@ cudaError_t launch_paged(const Paged &pp, void *ws, cudaStream_t st) {
     p.err = (uint32_t *)ws;
     PagedPlan w;
     paged_layout(p, ws, &w);
-    const bool run = p.T > 0 && p.n_seq > 0, tc = run && paged_tc_supported(p);
+    const bool run = p.T > 0 && p.n_seq > 0, tc = run && paged_tc_supported(p) && p.n_pages > 0;
     const int tab_ctas = tc ? std::min((p.T + 31) / 32, 296) : 0;
     count_launch();
     cudaError_t e = launch_pdl(k_paged_plan, dim3(1 + tab_ctas), dim3(1024), 0, st, p, w, tc ? 1 : 0, tab_ctas);

@@ -11,10 +11,12 @@ constexpr int kStepKeys = 64;   // keys of a step
 
 struct PagedHead {
     long long total, per;  // steps of all tiles; steps of a pair
+    int n_split;           // tiles that several pairs work on
 };
 struct PagedPlan {
     PagedHead *head;
     int *first;            // [kPairs] tile in which pair i begins
+    int *split;            // [kPairs] tiles that several pairs work on
     int4 *tiles;           // {sequence, first token, chunk of 128 heads, 0}
     long long *start;      // first step of a tile; one more entry: the total
     float2 *tab;           // [T, 32] (cos, sin) of the tokens' positions
@@ -39,7 +41,8 @@ __device__ __forceinline__ void tile_range(const Paged &p, const SeqView &v, int
 __device__ __forceinline__ int tile_steps(const Paged &p, const SeqView &v, int i0, int i1) {
     int lo, hi;
     tile_range(p, v, i0, i1, &lo, &hi);
-    return max(1, (int)(((long long)hi - lo + kStepKeys - 1) / kStepKeys));
+    // (the first step begins at a multiple of 8)
+    return max(1, (int)(((long long)hi - (lo & ~7) + kStepKeys - 1) / kStepKeys));
 }
 
 // Slot of key of sequence s, or -1 where its page is out of range.

@@ -13,15 +13,20 @@
 //
 // Step: S = Q K^T (128 x 64) in TMEM; softmax with a running maximum (the
 // output is rescaled only when it grows by more than 2^8); P, bf16, through
-// shared memory; O += P V, V the same key rows read MN-major. Keys are gathered
-// row by row from their pages, so a page may end anywhere; slots of keys that
-// no row of the tile sees are zero, and a row's weight of a key outside its own
-// range is zero. 8-bit rows become bf16 on the way (exact: a scale is a power
-// of two).
+// shared memory; O += P V, V the same key rows read MN-major. bf16 keys come by
+// TMA in groups of 8 rows where the tile sees all 8 and pages hold whole groups,
+// else row by row (TMA gathers of 4 rows x 64 columns, which need no groups, took
+// 64 cycles each and were twice as slow); 8-bit rows through registers, where they
+// become bf16 (exact: a scale is a power of two). Slots of keys that no row of the
+// tile sees are zero, and a row's weight of a key outside its own range is zero.
 //
-// What bounds it: long contexts, the keys' way from L2 (74 KB a step and CTA,
-// twice the cache's bytes over all) and the tensor work of 1000 cycles a step;
-// few keys, latency of the launches and of a step.
+// A CTA holds two steps of keys; the five slices that only S needs (the other
+// half's values, the rope keys) are free for the step after next once S is formed,
+// the other four once O is.
+//
+// What bounds it: long contexts, the tensor work (40 products of 64 keys take 50
+// cycles each, 4 of 256 columns 134: 2500 cycles a step) and the softmax beside
+// it; few keys, the latency of the launches, of Q and of a step.
 //
 // The query's turned rope slice is split as hi + lo of two bf16 (the cache's
 // rope keys are exact bf16 operands), so scores and LSE keep 2^-16.
@@ -29,8 +34,9 @@
 // TMEM: O 0..255, S 256..319, Q 320..511 (latent slices 0 - 3, rope hi, rope
 // lo). Shared: Q slices 4 - 7, two key stages, P.
 // Warps: 0-7 softmax (warps w and w + 4 share 32 rows and take 32 keys and 128
-// output columns each), 8-11 Q, 12-15 and 16-19 keys of even and odd steps, 20
-// MMA issue. Every wait is bounded.
+// output columns each); bf16: 8-11 Q, 12 keys, 13 and 14 issue the products of S
+// and of O; 8 bits: 8-11 keys of even steps and Q, 12-15 keys of odd steps, 16 and
+// 17 the products. Every wait is bounded.
 #include <algorithm>
 
 #include "dspark_latent_paged.cuh"
@@ -43,15 +49,19 @@ namespace {
 using namespace tc;
 
 constexpr int kDL = 512, kDR = 64;
-constexpr int kKSlice = kStepKeys * 128, kStage = 9 * kKSlice;
+// A stage: per group of 8 keys 1 KB (8 rows of 128 swizzled bytes) for each slice
+// of 64 columns; first the five slices that only S reads (the other half's, the
+// rope slice), group by group, then the CTA's own four.
+constexpr int kGroupA = 5 * 1024, kGroupB = 4 * 1024, oPartB = 8 * kGroupA, kStage = oPartB + 8 * kGroupB;
 constexpr int oQ = 2 * kStage, oP = oQ + 4 * 128 * 128;
 constexpr int oX = oP + 128 * 128;  // pair exchange [2][2][128]: maximum of a step, row sums of a segment
 constexpr int oBar = oX + 4 * 512;
-constexpr int kSmem = oBar + 256;
+constexpr int kSmem = oBar + 288;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320, kColR = kColQ + 4 * 32;
-constexpr int kSoft = 8, kWarpQ = 8, kWarpKeys = 12, kWarpM = 20;
-constexpr int kThreads = 21 * 32;
+constexpr int kSoft = 8, kWarpQ = 8, kWarpKeys = 12;
+constexpr int issuer_warp(int kind) { return kind == DSPARK_CACHE_BF16 ? 13 : 16; }  // of S; O's is the next
+constexpr int threads_of(int kind) { return (issuer_warp(kind) + 2) * 32; }
 constexpr float kGrow = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -59,6 +69,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct Seg {
     int seq, i0, n_tok, hc;     // tokens i0 .. i0 + n_tok of the sequence
     int tok0, kv, q_len, lo, hi;  // first token of q; keys; the tile's key range
+    int base;                     // key of the first step's first slot
     int s0, s1, slot;           // slot >= 0: a partial result
 };
 struct SegCursor {
@@ -84,6 +95,7 @@ struct SegCursor {
         g.kv = v.kv;
         g.q_len = v.q_len;
         tile_range(p, v, g.i0, g.i0 + g.n_tok, &g.lo, &g.hi);
+        g.base = g.lo & ~7;
         g.s0 = (int)(at - a);
         const long long e = min(end, b);
         g.s1 = (int)(e - a);
@@ -106,23 +118,96 @@ __device__ __forceinline__ uint32_t fp8x2_bf16(uint32_t w, float s) {
     return pack_bf16x2(f.x * s, f.y * s);
 }
 
+// The (token, head) of a tile's row.
+struct RowOf {
+    int ti, h;
+    bool live;
+    __device__ __forceinline__ RowOf(const Paged &p, const PagedPlan &w, const Seg &g, int r) {
+        ti = w.tpt > 1 || p.n_h == 128 ? r / p.n_h : 0;
+        h = g.hc * 128 + r - ti * p.n_h;
+        live = ti < g.n_tok && h < p.n_h && (ti == 0 || w.hchunks == 1);
+    }
+};
+
+// Row r of a segment's queries: latent slices 0 - 3 and the turned rope slice
+// into tensor memory, slices 4 - 7 into shared memory.
+__device__ __forceinline__ void load_q(const Paged &p, const PagedPlan &w, const Seg &sg, uint8_t *sm, uint32_t trow, int r) {
+    const RowOf o(p, w, sg, r);
+    const bool live = o.live;
+    const int tok = sg.tok0 + (live ? o.ti : 0);
+    const uint4 *src = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + (long long)tok * p.q_ts +
+                                                       (live ? o.h : 0) * p.q_hs);
+#pragma unroll
+    for (int c = 0; c < 32; c++) cp16(smem_u32(sm) + oQ + (c >> 3) * 16384 + sw128(r, c & 7), src + 32 + c, live);
+    tc_fence_after();
+    uint32_t x[32], lo[32];
+    auto load = [&](int c, uint32_t(&y)[32]) {
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            const uint4 v = live ? __ldg(src + 8 * c + u) : make_uint4(0, 0, 0, 0);
+            y[4 * u] = v.x;
+            y[4 * u + 1] = v.y;
+            y[4 * u + 2] = v.z;
+            y[4 * u + 3] = v.w;
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+        load(c, x);
+        load(c + 1, lo);
+        tmem_st32u(trow + kColQ + 32 * c, x);
+        tmem_st32u(trow + kColQ + 32 * c + 32, lo);
+    }
+    const float4 *tab = reinterpret_cast<const float4 *>(w.tab + (size_t)tok * 32);
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+        const uint4 v = live ? __ldg(src + kDL / 8 + u) : make_uint4(0, 0, 0, 0);
+        const float4 c0 = __ldg(tab + 2 * u), c1 = __ldg(tab + 2 * u + 1);
+        const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+        const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float a = __uint_as_float(wv[i] << 16), b = __uint_as_float(wv[i] & 0xffff0000u);
+            split_bf16x2(a * cs[i].x - b * cs[i].y, a * cs[i].y + b * cs[i].x, x[4 * u + i], lo[4 * u + i]);
+        }
+    }
+    tmem_st32u(trow + kColR, x);
+    tmem_st32u(trow + kColR + 32, lo);
+    tmem_wait_st();
+    tc_fence_before();
+    cp_wait_all();
+    fence_proxy_async_smem();
+}
+__device__ __forceinline__ void prefetch_q(const Paged &p, const PagedPlan &w, const Seg &sg, int r) {
+    const RowOf o(p, w, sg, r);
+    if (!o.live) return;
+    const __nv_bfloat16 *row = (const __nv_bfloat16 *)p.q + (long long)(sg.tok0 + o.ti) * p.q_ts + o.h * p.q_hs;
+    for (int i = 0; i < 9; i++) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64 * i));
+}
+
 template <int KIND>
-__global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const PagedPlan w) {
+__global__ void __launch_bounds__(threads_of(KIND), 1)
+    k_paged_tc(const __grid_constant__ CUtensorMap tm_k4, const __grid_constant__ CUtensorMap tm_k1, const Paged p, const PagedPlan w) {
+    constexpr int kWarpM = issuer_warp(KIND), kThreads = threads_of(KIND);
+    constexpr int kFull = KIND == DSPARK_CACHE_BF16 ? 2 : 4;  // arrivals for a part of a stage
     extern __shared__ __align__(1024) uint8_t sm[];  // swizzle atoms: no room for slack
-    uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + 2;
-    uint64_t *sfull = kempty + 2, *sfree = sfull + 1, *pready = sfull + 2, *pvdone = sfull + 3;
+    // of stage s: part 2 s the slices that only S reads, part 2 s + 1 those that O reads too
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + 4;
+    uint64_t *sfull = kempty + 4, *sfree = sfull + 1, *pready = sfull + 2, *pvdone = sfull + 3;
     uint64_t *qready = sfull + 4, *qfree = sfull + 5, *ofree = sfull + 6, *drain = sfull + 7;
-    uint64_t *xbar = sfull + 8, *lbar = xbar + 8;
+    uint64_t *xbar = sfull + 9, *lbar = xbar + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lbar + 4);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(lbar + 5);
-    volatile uint16_t *kmask = reinterpret_cast<volatile uint16_t *>(lbar + 6);  // [2][4]: the stage's valid keys
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(lbar + 4) + 1;
+    // [4][4]: 16 keys' validity each, of step g at g % 4 (a stage's first part is
+    // free before the softmax has read them)
+    volatile uint16_t *kmask = reinterpret_cast<volatile uint16_t *>(lbar + 5);
     float *xm = reinterpret_cast<float *>(sm + oX);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = blockIdx.x & 1;
     const uint64_t wlim = p.wait_ns;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; i++) {
-            mbar_init(&kfull[i], 4);
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&kfull[i], kFull);
             mbar_init(&kempty[i], 1);
         }
         mbar_init(sfull, 1);
@@ -132,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const P
         mbar_init(qready, 4);
         mbar_init(qfree, 1);
         mbar_init(ofree, kSoft);
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         for (int i = 0; i < 8; i++) mbar_init(&xbar[i], 2);
         for (int i = 0; i < 4; i++) mbar_init(&lbar[i], 2);
         *abort_flag = 0;
@@ -151,213 +237,251 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const P
     SegCursor cur;
     cur.begin(w);
     Seg sg;
+    uint32_t issued = 0;  // the TMA loader's parts of steps
 
-    if (warp >= kWarpKeys && warp < kWarpM) {
-        // ------------------------------------------------ keys -> stages
-        const int gp = (warp - kWarpKeys) >> 2, wr = (warp - kWarpKeys) & 3;  // stage; 16 rows from 16 wr
-        const uint32_t stage = smem_u32(sm) + gp * kStage;
-        uint32_t g = 0;
+    if (KIND == DSPARK_CACHE_BF16 && warp == kWarpKeys) {
+        // ------------------------------------------------- bf16 keys -> stages
+        if (lane == 0) tma_prefetch_desc(&tm_k4);
+        const bool groups = p.page_size % 8 == 0;
+        const uint8_t *cache = (const uint8_t *)p.cache;
         bool ok = true;
+        uint32_t g = 0;
         while (ok && cur.next(p, w, sg))
+            for (int t = sg.s0; ok && t < sg.s1; t++, g++) {
+                const int st = g & 1;
+                // lane l: the slots of keys l and l + 32 of the step
+                int row[2];
+                uint32_t valid[2];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int key = sg.base + t * kStepKeys + lane + 32 * i;
+                    long long slot = -1;
+                    if (key >= sg.lo && key < sg.hi) {
+                        slot = key_slot(p, sg.seq, key);
+                        if (slot < 0) atomicOr(p.err, kErrPage);
+                    }
+                    valid[i] = __ballot_sync(0xffffffffu, slot >= 0);
+                    row[i] = (int)slot;
+                }
+                // lane l < 8: whether group l is whole, and its first slot
+                const int ga = __shfl_sync(0xffffffffu, row[0], 8 * (lane & 3));
+                const int gb = __shfl_sync(0xffffffffu, row[1], 8 * (lane & 3));
+                const int gslot = lane & 4 ? gb : ga;
+                const bool whole = groups && ((lane & 4 ? valid[1] : valid[0]) >> (8 * (lane & 3)) & 0xffu) == 0xffu;
+                const uint32_t wholes = __ballot_sync(0xffffffffu, whole) & 0xffu;
+#pragma unroll
+                for (int part = 0; part < 2; part++) {
+                    if (g >= 2) ok = warp_all(mbar_wait(&kempty[2 * st + part], ((g >> 1) - 1) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    uint64_t *full = &kfull[2 * st + part];
+                    uint8_t *dst = sm + st * kStage + (part ? oPartB : 0);
+                    if (lane == 0) {
+                        if (part == 0) {
+                            kmask[(g & 3) * 4] = (uint16_t)valid[0];
+                            kmask[(g & 3) * 4 + 1] = (uint16_t)(valid[0] >> 16);
+                            kmask[(g & 3) * 4 + 2] = (uint16_t)valid[1];
+                            kmask[(g & 3) * 4 + 3] = (uint16_t)(valid[1] >> 16);
+                        }
+                        mbar_arrive_expect_tx(full, __popc(wholes) * (part ? kGroupB : kGroupA));
+                    }
+                    __syncwarp();
+                    issued = 2 * g + part + 1;
+                    if (lane < 8 && whole) {
+                        if (part == 0) {
+                            tma_load_3d(dst + lane * kGroupA, &tm_k4, full, 0, gslot, 4 * (half ^ 1));
+                            tma_load_3d(dst + lane * kGroupA + 4096, &tm_k1, full, 0, gslot, 8);
+                        } else {
+                            tma_load_3d(dst + lane * kGroupB, &tm_k4, full, 0, gslot, 4 * half);
+                        }
+                    }
+                    if (wholes != 0xffu) {
+                        // the other groups row by row: lane's row of a group, every fourth 16 bytes
+                        for (int gr = 0; gr < 8; gr++) {
+                            if ((wholes >> gr) & 1) continue;
+                            const int key = 8 * gr + (lane >> 2);
+                            const int a = __shfl_sync(0xffffffffu, row[0], key & 31);
+                            const int b = __shfl_sync(0xffffffffu, row[1], key & 31);
+                            const int slot = gr >= 4 ? b : a;
+                            const uint8_t *src = cache + (slot >= 0 ? (size_t)slot * p.row_bytes : 0);
+#pragma unroll
+                            for (int i = 0; i < 10; i++) {
+                                const int u = 4 * i + (lane & 3), n = u >> 3;  // unit of the part; its slice
+                                if (part == 1 && n >= 4) continue;
+                                const int c = part ? 4 * half + n : n == 4 ? 8 : 4 * (half ^ 1) + n;
+                                cp16(smem_u32(dst) + gr * (part ? kGroupB : kGroupA) + n * 1024 + sw128(lane >> 2, u & 7),
+                                     src + c * 128 + (u & 7) * 16, slot >= 0);
+                            }
+                        }
+                        cp_wait_all();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(full);
+                }
+            }
+    } else if (KIND == DSPARK_CACHE_FP8 && warp >= kWarpQ && warp < kWarpM) {
+        // -------------------------------------- 8-bit keys -> bf16 stages; Q
+        const int gp = (warp - kWarpQ) >> 2, wr = (warp - kWarpQ) & 3;  // stage; 16 rows from 16 wr
+        uint32_t g = 0, k = 0;
+        bool ok = true;
+        for (; ok && cur.next(p, w, sg); k++) {
+            if (gp == 0) {
+                const int r = wr * 32 + lane;
+                if (k > 0) {
+                    prefetch_q(p, w, sg, r);
+                    ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
+                }
+                if (!ok) break;
+                load_q(p, w, sg, sm, tmem + ((uint32_t)(wr * 32) << 16), r);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qready);
+            }
             for (int t = sg.s0; ok && t < sg.s1; t++, g++) {
                 if ((int)(g & 1) != gp) continue;
                 // lane l < 16: the slot of key 16 wr + l of the step
-                const int key = sg.lo + t * kStepKeys + 16 * wr + (lane & 15);
+                const int key = sg.base + t * kStepKeys + 16 * wr + (lane & 15);
                 long long slot = -1;
-                if (key < sg.hi) {
+                if (key >= sg.lo && key < sg.hi) {
                     slot = key_slot(p, sg.seq, key);
                     if (slot < 0 && lane < 16) atomicOr(p.err, kErrPage);
                 }
                 const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0) & 0xffffu;
-                if (g >= 2) ok = warp_all(mbar_wait(&kempty[gp], ((g >> 1) - 1) & 1, abort_flag, wlim));
-                if (!ok) break;
-                if (lane == 0) kmask[gp * 4 + wr] = (uint16_t)valid;
                 const uint8_t *cache = (const uint8_t *)p.cache;
                 const long long off = slot >= 0 ? slot * (long long)p.row_bytes : -1;
-                if constexpr (KIND == DSPARK_CACHE_BF16) {
-#pragma unroll 6
-                    for (int i = 0; i < 36; i++) {
-                        const int e = lane + 32 * i, row = e / 72, ch = e % 72;
-                        const long long o = __shfl_sync(0xffffffffu, off, row);
-                        cp16(stage + (ch >> 3) * kKSlice + sw128(16 * wr + row, ch & 7), cache + (o >= 0 ? o + ch * 16 : 0),
-                             o >= 0);
-                    }
-                } else {
-                    // lane: rows 8 rb + lane / 4, 16 codes of each slice; the rope slice as it is
+                // lane: rows 8 rb + lane / 4, 16 codes of each slice
+                uint4 x[2][8];
+                float4 sc[2];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int row = 4 * i + (lane >> 3), ch = lane & 7;
-                        const long long o = __shfl_sync(0xffffffffu, off, row);
-                        cp16(stage + 8 * kKSlice + sw128(16 * wr + row, ch), cache + (o >= 0 ? o + kDL + ch * 16 : 0),
-                             o >= 0);
+                for (int rb = 0; rb < 2; rb++) {
+                    const long long o = __shfl_sync(0xffffffffu, off, 8 * rb + (lane >> 2));
+                    const uint8_t *row = cache + (o >= 0 ? o : 0);
+                    sc[rb] = o >= 0 ? __ldg(reinterpret_cast<const float4 *>(row + kDL + 2 * kDR))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int s = 0; s < 8; s++)
+                        x[rb][s] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * s + 16 * (lane & 3)))
+                                          : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int part = 0; part < 2; part++) {
+                    if (g >= 2) ok = warp_all(mbar_wait(&kempty[2 * gp + part], ((g >> 1) - 1) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    if (part == 0) {
+                        if (lane == 0) kmask[(g & 3) * 4 + wr] = (uint16_t)valid;
+                        // the rope slice as it is
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int row = 4 * i + (lane >> 3), ch = lane & 7;
+                            const long long o = __shfl_sync(0xffffffffu, off, row);
+                            cp16(smem_u32(sm) + gp * kStage + (2 * wr + (row >> 3)) * kGroupA + 4096 + sw128(row & 7, ch),
+                                 cache + (o >= 0 ? o + kDL + ch * 16 : 0), o >= 0);
+                        }
                     }
-                    uint4 x[2][8];
-                    float4 sc[2];
+                    const bool upper = (half ^ part ^ 1) != 0;  // slices 4 - 7 or 0 - 3
 #pragma unroll
                     for (int rb = 0; rb < 2; rb++) {
-                        const long long o = __shfl_sync(0xffffffffu, off, 8 * rb + (lane >> 2));
-                        const uint8_t *row = cache + (o >= 0 ? o : 0);
-                        sc[rb] = o >= 0 ? __ldg(reinterpret_cast<const float4 *>(row + kDL + 2 * kDR))
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                        uint8_t *dst = sm + gp * kStage + (part ? oPartB + (2 * wr + rb) * kGroupB : (2 * wr + rb) * kGroupA);
 #pragma unroll
-                        for (int s = 0; s < 8; s++)
-                            x[rb][s] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * s + 16 * (lane & 3)))
-                                              : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int rb = 0; rb < 2; rb++) {
-                        const int row = 16 * wr + 8 * rb + (lane >> 2);
-#pragma unroll
-                        for (int s = 0; s < 8; s++) {
-                            const float f = s < 2 ? sc[rb].x : s < 4 ? sc[rb].y : s < 6 ? sc[rb].z : sc[rb].w;
-                            const uint4 v = x[rb][s];
-                            uint8_t *dst = sm + gp * kStage + s * kKSlice;
-                            *reinterpret_cast<uint4 *>(dst + sw128(row, 2 * (lane & 3))) =
+                        for (int n = 0; n < 4; n++) {
+                            const float f = upper ? (n < 2 ? sc[rb].z : sc[rb].w) : (n < 2 ? sc[rb].x : sc[rb].y);
+                            const uint4 a = x[rb][n], b = x[rb][4 + n];
+                            const uint4 v = make_uint4(upper ? b.x : a.x, upper ? b.y : a.y, upper ? b.z : a.z,
+                                                       upper ? b.w : a.w);
+                            *reinterpret_cast<uint4 *>(dst + n * 1024 + sw128(lane >> 2, 2 * (lane & 3))) =
                                 make_uint4(fp8x2_bf16(v.x, f), fp8x2_bf16(v.x >> 16, f), fp8x2_bf16(v.y, f),
                                            fp8x2_bf16(v.y >> 16, f));
-                            *reinterpret_cast<uint4 *>(dst + sw128(row, 2 * (lane & 3) + 1)) =
+                            *reinterpret_cast<uint4 *>(dst + n * 1024 + sw128(lane >> 2, 2 * (lane & 3) + 1)) =
                                 make_uint4(fp8x2_bf16(v.z, f), fp8x2_bf16(v.z >> 16, f), fp8x2_bf16(v.w, f),
                                            fp8x2_bf16(v.w >> 16, f));
                         }
                     }
+                    if (part == 0) cp_wait_all();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kfull[2 * gp + part]);
                 }
-                cp_wait_all();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kfull[gp]);
             }
+        }
         cp_wait_all();
-    } else if (warp >= kWarpQ && warp < kWarpKeys) {
+    } else if (KIND == DSPARK_CACHE_BF16 && warp >= kWarpQ && warp < kWarpKeys) {
         // -------------------------------------- Q -> shared and tensor memory
         const int r = (warp - kWarpQ) * 32 + lane;
-        const uint32_t trow = tmem + ((uint32_t)((warp - kWarpQ) * 32) << 16);
         uint32_t k = 0;  // segments
         bool ok = true;
         for (; ok && cur.next(p, w, sg); k++) {
-            const int ti = w.tpt > 1 || p.n_h == 128 ? r / p.n_h : 0, h = sg.hc * 128 + r - ti * p.n_h;
-            const bool live = ti < sg.n_tok && h < p.n_h && (ti == 0 || w.hchunks == 1);
-            const int tok = sg.tok0 + (live ? ti : 0);
-            const __nv_bfloat16 *row = (const __nv_bfloat16 *)p.q + (long long)tok * p.q_ts + (live ? h : 0) * p.q_hs;
-            const uint4 *src = reinterpret_cast<const uint4 *>(row);
-            if (k > 0) {
-                if (live)
-                    for (int i = 0; i < 9; i++) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * i));
-                ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
-            }
+            prefetch_q(p, w, sg, r);
+            if (k > 0) ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
             if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < 32; c++)
-                cp16(smem_u32(sm) + oQ + (c >> 3) * 16384 + sw128(r, c & 7), src + 32 + c, live);
-            tc_fence_after();
-            uint32_t x[32], lo[32];
-#pragma unroll 1
-            for (int c = 0; c < 4; c++) {
-#pragma unroll
-                for (int u = 0; u < 8; u++) {
-                    const uint4 v = live ? __ldg(src + 8 * c + u) : make_uint4(0, 0, 0, 0);
-                    x[4 * u] = v.x;
-                    x[4 * u + 1] = v.y;
-                    x[4 * u + 2] = v.z;
-                    x[4 * u + 3] = v.w;
-                }
-                tmem_st32u(trow + kColQ + 32 * c, x);
-            }
-            const float4 *tab = reinterpret_cast<const float4 *>(w.tab + (size_t)tok * 32);
-#pragma unroll
-            for (int u = 0; u < 8; u++) {
-                const uint4 v = live ? __ldg(src + kDL / 8 + u) : make_uint4(0, 0, 0, 0);
-                const float4 c0 = __ldg(tab + 2 * u), c1 = __ldg(tab + 2 * u + 1);
-                const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
-                const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float a = __uint_as_float(wv[i] << 16), b = __uint_as_float(wv[i] & 0xffff0000u);
-                    split_bf16x2(a * cs[i].x - b * cs[i].y, a * cs[i].y + b * cs[i].x, x[4 * u + i], lo[4 * u + i]);
-                }
-            }
-            tmem_st32u(trow + kColR, x);
-            tmem_st32u(trow + kColR + 32, lo);
-            tmem_wait_st();
-            tc_fence_before();
-            cp_wait_all();
-            fence_proxy_async_smem();
+            load_q(p, w, sg, sm, tmem + ((uint32_t)((warp - kWarpQ) * 32) << 16), r);
             __syncwarp();
             if (lane == 0) mbar_arrive(qready);
         }
         cp_wait_all();
     } else if (warp == kWarpM) {
-        // ---------------------------------------------------------- MMAs
+        // ------------------------------------------------------ S = Q K^T
         if (lane == 0) {
-            const uint32_t idS = idesc_bf16(128, kStepKeys, 0), idO = idesc_bf16(128, 256, 1);
-            SegCursor cv = cur;
-            Seg sv;
-            bool hq = cur.next(p, w, sg), hv = cv.next(p, w, sv), ok = true;
-            int tq = hq ? sg.s0 : 0, tv = hv ? sv.s0 : 0;
-            uint32_t gq = 0, gv = 0, kq = 0, kv = 0;  // steps and segments of the two cursors
-            const SDesc pd = sdesc_split(sdesc_sw128(smem_u32(sm + oP), 16, 1024));
-            uint64_t idle = 0;
-            while (ok && hv) {
-                bool issued = false;
-                if (hq && (tq != sg.s0 || mbar_test(qready, kq & 1)) && mbar_test(&kfull[gq & 1], (gq >> 1) & 1) &&
-                    (gq == 0 || mbar_test(sfree, (gq - 1) & 1))) {
-                    tc_fence_after();
-                    const uint32_t kb = smem_u32(sm) + (gq & 1) * kStage;
-                    const SDesc kd = sdesc_split(sdesc_sw128(kb, 16, 1024));
-                    const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oQ), 16, 1024));
-                    const uint32_t dS = tmem + kColS;
+            const uint32_t idS = idesc_bf16(128, kStepKeys, 0), dS = tmem + kColS;
+            const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oQ), 16, 1024));
+            uint32_t g = 0, k = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
+            // latent slices 0 - 3 (Q in tensor memory) or 4 - 7 (Q in shared memory); kd: the first of the four
+            auto four = [&](const SDesc &kd, bool upper, bool first) {
+                if (upper) {
 #pragma unroll
-                    for (int c = 0; c < 8; c++)
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const uint64_t b = kd.at(c * (kKSlice / 16) + 2 * k);
-                            if (c < 4) mma_bf16_ts(dS, tmem + kColQ + 32 * c + 8 * k, b, idS, (c | k) != 0 ? 1u : 0u);
-                            else mma_bf16_ss(dS, qd.at((c - 4) * 1024 + 2 * k), b, idS, 1u);
-                        }
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const uint64_t b = kd.at(8 * (kKSlice / 16) + 2 * k);
-                        mma_bf16_ts(dS, tmem + kColR + 8 * k, b, idS, 1u);
-                        mma_bf16_ts(dS, tmem + kColR + 32 + 8 * k, b, idS, 1u);
-                    }
-                    gq++;
-                    if (++tq == sg.s1) {
-                        mma_commit(qfree);
-                        kq++;
-                        hq = cur.next(p, w, sg);
-                        if (hq) tq = sg.s0;
-                    }
-                    mma_commit(sfull);
-                    issued = true;
-                }
-                if (gv < gq && mbar_test(pready, gv & 1) && (tv != sv.s0 || kv == 0 || mbar_test(ofree, (kv - 1) & 1))) {
-                    tc_fence_after();
-                    const uint32_t vb = smem_u32(sm) + (gv & 1) * kStage + 4 * half * kKSlice;
-                    const SDesc vd = sdesc_split(sdesc_sw128(vb, kKSlice, 1024));
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma_bf16_ss(tmem + kColO, pd.at(2 * k), vd.at(128 * k), idO, tv != sv.s0 || k > 0 ? 1u : 0u);
-                    mma_commit(&kempty[gv & 1]);
-                    mma_commit(pvdone);
-                    gv++;
-                    if (++tv == sv.s1) {
-                        kv++;
-                        hv = cv.next(p, w, sv);
-                        if (hv) tv = sv.s0;
-                    }
-                    issued = true;
-                }
-                if (issued) {
-                    idle = 0;
+                    for (int n = 0; n < 16; n++)
+                        mma_bf16_ss(dS, qd.at((n >> 2) * 1024 + 2 * (n & 3)), kd.at((n >> 2) * 64 + 2 * (n & 3)), idS,
+                                    !first || n > 0);
                 } else {
-                    const uint64_t now = globaltimer();
-                    if (idle == 0) idle = now;
-                    if (*abort_flag) ok = false;
-                    else if (now - idle > wlim) {
-                        *abort_flag = 1;
-                        ok = false;
-                    }
+#pragma unroll
+                    for (int n = 0; n < 16; n++)
+                        mma_bf16_ts(dS, tmem + kColQ + 8 * n, kd.at((n >> 2) * 64 + 2 * (n & 3)), idS, !first || n > 0);
                 }
-            }
+            };
+            for (; ok && cur.next(p, w, sg); k++)
+                for (int t = sg.s0; t < sg.s1; t++, g++) {
+                    const int st = g & 1;
+                    if (t == sg.s0 && !wait(qready, k & 1)) break;
+                    if (g > 0 && !wait(sfree, (g - 1) & 1)) break;
+                    if (!wait(&kfull[2 * st], (g >> 1) & 1)) break;
+                    tc_fence_after();
+                    const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage, 16, kGroupA));
+                    four(kd, half == 0, true);
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        const uint64_t b = kd.at(4 * 64 + 2 * u);
+                        mma_bf16_ts(dS, tmem + kColR + 8 * u, b, idS, 1u);
+                        mma_bf16_ts(dS, tmem + kColR + 32 + 8 * u, b, idS, 1u);
+                    }
+                    mma_commit(&kempty[2 * st]);
+                    if (!wait(&kfull[2 * st + 1], (g >> 1) & 1)) break;
+                    tc_fence_after();
+                    four(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 16, kGroupB)), half != 0, false);
+                    if (t + 1 == sg.s1) mma_commit(qfree);
+                    mma_commit(sfull);
+                }
+        }
+    } else if (warp == kWarpM + 1) {
+        // ------------------------------------------------------- O += P V
+        if (lane == 0) {
+            const uint32_t idO = idesc_bf16(128, 256, 1);
+            const SDesc pd = sdesc_split(sdesc_sw128(smem_u32(sm + oP), 16, 1024));
+            uint32_t g = 0, k = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
+            for (; ok && cur.next(p, w, sg); k++)
+                for (int t = sg.s0; t < sg.s1; t++, g++) {
+                    const int st = g & 1;
+                    if (!wait(pready, g & 1) || (t == sg.s0 && k > 0 && !wait(ofree, (k - 1) & 1))) break;
+                    tc_fence_after();
+                    const SDesc vd =
+                        sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 1024, kGroupB));
+#pragma unroll
+                    for (int u = 0; u < 4; u++)
+                        mma_bf16_ss(tmem + kColO, pd.at(2 * u), vd.at(2 * (kGroupB / 16) * u), idO, t != sg.s0 || u > 0 ? 1u : 0u);
+                    mma_commit(&kempty[2 * st + 1]);
+                    mma_commit(pvdone);
+                }
         }
     } else {
         // -------------------------------------------------------- softmax
@@ -366,8 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const P
         uint32_t g = 0, sk = 0;
         bool ok = true;
         for (; ok && cur.next(p, w, sg); sk++) {
-            const int ti = w.tpt > 1 || p.n_h == 128 ? r / p.n_h : 0, h = sg.hc * 128 + r - ti * p.n_h;
-            const bool live = ti < sg.n_tok && h < p.n_h && (ti == 0 || w.hchunks == 1);
+            const RowOf row(p, w, sg, r);
+            const int ti = row.ti, h = row.h;
+            const bool live = row.live;
             const SeqView v{sg.tok0 - sg.i0, sg.q_len, sg.kv, false};
             int lo = 0, hi = 0;
             if (live) seq_range(p, v, sg.i0 + ti, &lo, &hi);
@@ -379,12 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const P
                 tc_fence_after();
                 float s[32];
                 tmem_ld32(trow + kColS + 32 * hf, s);
-                const uint32_t km = kmask[(g & 1) * 4 + 2 * hf] | ((uint32_t)kmask[(g & 1) * 4 + 2 * hf + 1] << 16);
+                const uint32_t km = kmask[(g & 3) * 4 + 2 * hf] | ((uint32_t)kmask[(g & 3) * 4 + 2 * hf + 1] << 16);
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sfree);
-                const int k0 = sg.lo + t * kStepKeys + 32 * hf;
+                const int k0 = sg.base + t * kStepKeys + 32 * hf;
                 const int c0 = max(lo - k0, 0), c1 = min(hi - k0, 32);
                 uint32_t rm = c1 > c0 ? (c1 >= 32 ? 0xffffffffu : (1u << c1) - 1u) & ~((1u << (c0 & 31)) - 1u) : 0u;
                 rm &= km;
@@ -517,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const P
                 const int who = __ffs(redo) - 1;
                 redo &= redo - 1;
                 const int rti = __shfl_sync(0xffffffffu, ti, who), rh = __shfl_sync(0xffffffffu, h, who);
-                const int ka = max(__shfl_sync(0xffffffffu, lo, who), sg.lo + sg.s0 * kStepKeys);
-                const int kb = min(__shfl_sync(0xffffffffu, hi, who), sg.lo + sg.s1 * kStepKeys);
+                const int ka = max(__shfl_sync(0xffffffffu, lo, who), sg.base + sg.s0 * kStepKeys);
+                const int kb = min(__shfl_sync(0xffffffffu, hi, who), sg.base + sg.s1 * kStepKeys);
                 const int rtok = sg.tok0 + rti;
                 float acc[18], rmx, rl;
                 paged_row<__nv_bfloat16, KIND, 18, 1>(
@@ -547,10 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const P
 
     // ---------------------------------------------------------- teardown
     __syncthreads();
-    if (*abort_flag && warp == kWarpM && lane == 0) {
+    if (*abort_flag && lane == 0) {
         volatile int never = 0;
-        mma_commit(drain);
-        mbar_wait(drain, 0, &never);
+        if (KIND == DSPARK_CACHE_BF16 && warp == kWarpKeys)
+            for (uint32_t n = issued > 4 ? issued - 4 : 0; n < issued; n++)  // part n % 2 of step n / 2
+                mbar_wait(&kfull[n & 3], (n >> 2) & 1, &never);
+        if (warp >= kWarpM) {
+            mma_commit(&drain[warp - kWarpM]);
+            mbar_wait(&drain[warp - kWarpM], 0, &never);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -561,24 +691,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tc(const Paged p, const P
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
 }
 
-// Joins the parts of the tiles that pairs shared. CTA (i, y): the tile that
-// pair i goes on with and pair i - 1 began, rows y, y + gridDim.y, ...; four
+// Joins the parts of the tiles that pairs shared, a row to a CTA at a time; four
 // groups of 128 threads take every fourth part, four columns to a thread.
 __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPlan w) {
     __shared__ float wt[kPairs + 1];
     __shared__ float4 sum[3][128];
     pdl_wait();
-    const long long per = w.head->per, total = w.head->total, b = per * (blockIdx.x + 1);
-    if (b >= total) return;
-    const int r = w.first[blockIdx.x + 1];
-    // first[] names the tile at the pair's first step: one that begins there is not shared
-    const long long t0 = w.start[r], t1 = w.start[r + 1];
-    if (t0 >= b || t0 / per != blockIdx.x) return;
-    const int4 tl = w.tiles[r];
-    const SeqView v = seq_view(p, tl.x);
-    const int p0 = blockIdx.x, n = (int)((t1 - 1) / per) - p0 + 1;
-    const int grp = threadIdx.x >> 7, c = threadIdx.x & 127;
-    for (int row = blockIdx.y; row < 128; row += gridDim.y) {
+    const long long per = w.head->per;
+    const int units = w.head->n_split * 128;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int r = w.split[u >> 7], row = u & 127;
+        const long long t0 = w.start[r], t1 = w.start[r + 1];
+        const int4 tl = w.tiles[r];
+        const SeqView v = seq_view(p, tl.x);
+        const int p0 = (int)(t0 / per), n = (int)((t1 - 1) / per) - p0 + 1;
+        const int grp = threadIdx.x >> 7, c = threadIdx.x & 127;
         const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.z * 128 + row - ti * p.n_h;
         if (ti >= min(w.tpt, v.q_len - tl.y) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
         // part k: pair p0 + k, its slot 1 for the tile's beginning, 0 after it
@@ -590,7 +717,7 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (m != -INFINITY) {
             for (int k = 0; k < n; k++) l += exp2f(wt[k] - m);
-#pragma unroll 4
+#pragma unroll 8
             for (int k = grp; k < n; k += 4) {
                 const float4 x = __ldg(reinterpret_cast<const float4 *>(
                                            w.part_o + ((size_t)(2 * (p0 + k) + (k == 0)) * 128 + row) * kDL) + c);
@@ -619,20 +746,29 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
     }
 }
 
-template <int KIND> cudaError_t launch_t(const Paged &p, const PagedPlan &w, cudaStream_t st) {
+template <int KIND>
+cudaError_t launch_t(const CUtensorMap &m4, const CUtensorMap &m1, const Paged &p, const PagedPlan &w, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(k_paged_tc<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     count_launch();
-    return launch_pdl(k_paged_tc<KIND>, dim3(2 * kPairs), dim3(kThreads), kSmem, st, p, w);
+    return launch_pdl(k_paged_tc<KIND>, dim3(2 * kPairs), dim3(threads_of(KIND)), kSmem, st, m4, m1, p, w);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tc(const Paged &p, const PagedPlan &w, cudaStream_t st) {
-    cudaError_t e = p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(p, w, st) : launch_t<DSPARK_CACHE_FP8>(p, w, st);
+    // 64 columns, slots, slices of 64 columns
+    CUtensorMap m4{}, m1{};
+    const uint64_t dims[3] = {64, (uint64_t)p.n_pages * p.page_size, 9}, strides[2] = {(kDL + kDR) * 2, 128};
+    const uint32_t b4[3] = {64, 8, 4}, b1[3] = {64, 8, 1};
+    if (p.kind == DSPARK_CACHE_BF16 &&
+        (!make_map_nd(&m4, p.cache, 3, dims, strides, b4) || !make_map_nd(&m1, p.cache, 3, dims, strides, b1)))
+        return cudaErrorInvalidValue;
+    cudaError_t e = p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(m4, m1, p, w, st)
+                                                : launch_t<DSPARK_CACHE_FP8>(m4, m1, p, w, st);
     if (e != cudaSuccess) return e;
     count_launch();
-    return launch_pdl(k_paged_join, dim3(kPairs - 1, 16), dim3(512), 0, st, p, w);
+    return launch_pdl(k_paged_join, dim3(296), dim3(512), 0, st, p, w);
 }
 
 }  // namespace dspark

@@ -136,8 +136,8 @@ DSPARK_API dspark_status dspark_latent_cache_read(const dspark_latent_cache *p, 
  * A row that sees no key gives O = 0, LSE = -inf. Rows of o and lse behind the
  * last sequence's tokens are left as they were.
  *   q [T, n_h, d_l + d_r], o [T, n_h, d_l]: dtype, rope slice last and NOT
- *     rotated, with the given strides in elements (multiples of 16 bytes; both 0
- *     = contiguous); lse [T, n_h] fp32 contiguous
+ *     rotated, with the given strides in elements (multiples of 16 bytes, positive
+ *     and below 2^39; both 0 = contiguous); lse [T, n_h] fp32 contiguous
  *   q_start [n_seq + 1], kv_len [n_seq], block_table [n_seq, max_pages]: int32
  * A page outside [0, n_pages), a kv_len outside [0, max_pages * page_size] or a
  * q_start that is not ascending within [0, T] is only visible on the device: the

@@ -131,10 +131,11 @@ dspark_status make_paged(const dspark_latent_paged *pp, Paged *out) {
         r.o_ts = (long long)p.n_h * p.d_l;
         r.o_hs = p.d_l;
     }
-    if (r.q_ts < 0 || r.q_hs < 0 || r.o_ts < 0 || r.o_hs < 0) return DSPARK_ERR_SHAPE;
+    if (r.q_ts < 0 || r.q_hs < 0 || r.o_ts < 0 || r.o_hs < 0 || (r.q_ts == 0 && p.T > 1) || (r.q_hs == 0 && p.n_h > 1))
+        return DSPARK_ERR_SHAPE;
     if (r.q_ts % per16 || r.q_hs % per16 || r.o_ts % per16 || r.o_hs % per16) return DSPARK_ERR_ALIGN;
     // strides far outside any tensor would overflow the address arithmetic
-    const long long far = 1ll << 40;
+    const long long far = 1ll << 39;
     if (r.q_ts >= far || r.q_hs >= far || r.o_ts >= far || r.o_hs >= far) return DSPARK_ERR_UNSUPPORTED;
     // output rows must not overlap: tokens apart by more than a token's heads reach, or the reverse
     const bool tok_major = (p.T <= 1 || r.o_ts >= (long long)(p.n_h - 1) * r.o_hs + p.d_l) &&

@@ -12,7 +12,7 @@ namespace {
 // for a q_start or kv_len out of range, else 0; pages are checked by the
 // kernels that read them) and, for the tensor-core kernel, the list of row
 // tiles: tile r is up to 128 (token, head) rows of one sequence and takes
-// start[r + 1] - start[r] steps of 64 keys, at least one. The CTA pairs of the
+// its steps of 64 keys, at least one. The CTA pairs of the
 // attention share all steps evenly, wherever tiles begin and end; first[i] is
 // the tile that pair i begins in. The other CTAs fill the tokens' (cos, sin).
 __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedPlan w, int tc, int tab_ctas) {
@@ -99,9 +99,18 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
                 bad = 1;
                 break;
             }
-            w.tiles[bt + t] = make_int4(s, i0, hc, 0);
-            w.start[bt + t] = bs;
-            bs += tile_steps(p, v, i0, min(v.q_len, i0 + w.tpt));
+            PagedTile o;
+            o.seq = s;
+            o.i0 = i0;
+            o.hc = hc;
+            o.q_len = v.q_len;
+            o.q0 = v.q0;
+            o.kv = v.kv;
+            tile_range(p, v, i0, min(v.q_len, i0 + w.tpt), &o.lo, &o.hi);
+            o.start = bs;
+            o.steps = tile_steps(p, v, i0, min(v.q_len, i0 + w.tpt));
+            w.tiles[bt + t] = o;
+            bs += o.steps;
         }
         __syncthreads();
     }
@@ -114,12 +123,11 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         if (threadIdx.x == 0) {
             w.head->total = total;
             w.head->per = X;
-            w.start[total ? n : 0] = total;
         }
         __syncthreads();
         if (total)
             for (int r = threadIdx.x; r < n; r += blockDim.x) {
-                const long long a = w.start[r], b = w.start[r + 1];
+                const long long a = w.tiles[r].start, b = a + w.tiles[r].steps;
                 for (long long i = (a + X - 1) / X; i < kPairs && i * X < b; i++) w.first[i] = r;
                 if (a / X != (b - 1) / X) w.split[atomicAdd(&n_split, 1)] = r;  // (at most one for each end of a pair)
             }
@@ -151,8 +159,7 @@ size_t paged_layout(const Paged &p, void *ws, PagedPlan *w) {
     };
     r.first = (int *)take(sizeof(int) * kPairs);
     r.split = (int *)take(sizeof(int) * kPairs);
-    r.tiles = (int4 *)take(sizeof(int4) * ((size_t)r.max_tiles + 1));
-    r.start = (long long *)take(sizeof(long long) * ((size_t)r.max_tiles + 1));
+    r.tiles = (PagedTile *)take(sizeof(PagedTile) * (size_t)r.max_tiles);
     r.tab = (float2 *)take(sizeof(float2) * 32 * (size_t)p.T);
     r.part_lse = (float *)take(sizeof(float) * 2 * kPairs * 128);
     r.part_o = (float *)take(sizeof(float) * 2 * kPairs * 128 * 512);

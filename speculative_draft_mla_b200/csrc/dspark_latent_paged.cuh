@@ -13,12 +13,16 @@ struct PagedHead {
     long long total, per;  // steps of all tiles; steps of a pair
     int n_split;           // tiles that several pairs work on
 };
+struct alignas(16) PagedTile {      // up to 128 (token, head) rows of a sequence
+    int seq, i0, hc, q_len;  // first token within the sequence, chunk of 128 heads
+    int q0, kv, lo, hi;      // the sequence's first token; keys; keys that some row sees
+    long long start, steps;  // its steps in the list of all
+};
 struct PagedPlan {
     PagedHead *head;
     int *first;            // [kPairs] tile in which pair i begins
     int *split;            // [kPairs] tiles that several pairs work on
-    int4 *tiles;           // {sequence, first token, chunk of 128 heads, 0}
-    long long *start;      // first step of a tile; one more entry: the total
+    PagedTile *tiles;
     float2 *tab;           // [T, 32] (cos, sin) of the tokens' positions
     float *part_lse, *part_o;  // [2 kPairs, 128], [2 kPairs, 128, 512]: results of parts of a tile
     int tpt, hchunks, max_tiles;  // tokens of a tile, its chunks of heads

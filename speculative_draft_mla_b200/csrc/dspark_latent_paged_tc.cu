@@ -56,7 +56,7 @@ constexpr int kGroupA = 5 * 1024, kGroupB = 4 * 1024, oPartB = 8 * kGroupA, kSta
 constexpr int oQ = 2 * kStage, oP = oQ + 4 * 128 * 128;
 constexpr int oX = oP + 128 * 128;  // pair exchange [2][2][128]: maximum of a step, row sums of a segment
 constexpr int oBar = oX + 4 * 512;
-constexpr int kSmem = oBar + 288;
+constexpr int kSmem = oBar + 304;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320, kColR = kColQ + 4 * 32;
 constexpr int kSoft = 8, kWarpQ = 8, kWarpKeys = 12;
@@ -67,38 +67,37 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // A part of a tile that a pair works on: steps [s0, s1) of it.
 struct Seg {
-    int seq, i0, n_tok, hc;     // tokens i0 .. i0 + n_tok of the sequence
+    int seq, i0, n_tok, hc;       // tokens i0 .. i0 + n_tok of the sequence
     int tok0, kv, q_len, lo, hi;  // first token of q; keys; the tile's key range
     int base;                     // key of the first step's first slot
-    int s0, s1, slot;           // slot >= 0: a partial result
+    int s0, s1, slot;             // slot >= 0: a partial result
 };
 struct SegCursor {
     long long at, end, per;
     int r, pair;
     __device__ __forceinline__ void begin(const PagedPlan &w) {
         pair = blockIdx.x >> 1;
+        r = w.first[pair];  // (not written where the pair has no steps)
         per = w.head->per;
         at = per * pair;
         end = min(at + per, w.head->total);
-        r = at < end ? w.first[pair] : 0;
     }
     __device__ __forceinline__ bool next(const Paged &p, const PagedPlan &w, Seg &g) {
         if (at >= end) return false;
-        const int4 t = w.tiles[r];
-        const long long a = w.start[r], b = w.start[r + 1];
-        const SeqView v = seq_view(p, t.x);
-        g.seq = t.x;
-        g.i0 = t.y;
-        g.hc = t.z;
-        g.n_tok = min(w.tpt, v.q_len - t.y);
-        g.tok0 = v.q0 + t.y;
-        g.kv = v.kv;
-        g.q_len = v.q_len;
-        tile_range(p, v, g.i0, g.i0 + g.n_tok, &g.lo, &g.hi);
-        g.base = g.lo & ~7;
-        g.s0 = (int)(at - a);
-        const long long e = min(end, b);
-        g.s1 = (int)(e - a);
+        const PagedTile t = w.tiles[r];
+        g.seq = t.seq;
+        g.i0 = t.i0;
+        g.hc = t.hc;
+        g.n_tok = min(w.tpt, t.q_len - t.i0);
+        g.tok0 = t.q0 + t.i0;
+        g.kv = t.kv;
+        g.q_len = t.q_len;
+        g.lo = t.lo;
+        g.hi = t.hi;
+        g.base = t.lo & ~7;
+        g.s0 = (int)(at - t.start);
+        const long long b = t.start + t.steps, e = min(end, b);
+        g.s1 = (int)(e - t.start);
         g.slot = g.s0 == 0 && e == b ? -1 : 2 * pair + (g.s0 == 0 ? 1 : 0);
         at = e;
         r++;
@@ -129,39 +128,31 @@ struct RowOf {
     }
 };
 
-// Row r of a segment's queries: latent slices 0 - 3 and the turned rope slice
-// into tensor memory, slices 4 - 7 into shared memory.
-__device__ __forceinline__ void load_q(const Paged &p, const PagedPlan &w, const Seg &sg, uint8_t *sm, uint32_t trow, int r) {
+// A segment's queries, by four warps (thread = row r of 128). TMA brings latent
+// slices 0 - 3 into Q's shared memory (rows one to a lane would cost a request
+// each), from where they go to tensor memory; then slices 4 - 7 come to stay. The
+// rope slice is turned on its way to tensor memory. land: both copies' barrier.
+__device__ __forceinline__ bool load_q(const Paged &p, const PagedPlan &w, const Seg &sg, const CUtensorMap *tm, uint8_t *sm,
+                                       uint32_t tmem, int wr, uint32_t bytes, uint64_t *land, uint64_t *read, uint64_t *ready,
+                                       uint32_t k, uint32_t &armed, volatile int *abort_flag, uint64_t wlim) {
+    const int lane = threadIdx.x & 31, r = wr * 32 + lane, h0 = sg.hc * 128;
+    const uint32_t trow = tmem + ((uint32_t)(wr * 32) << 16);
+    if (wr == 0 && lane == 0) {
+        mbar_arrive_expect_tx(land, 4 * bytes);
+        armed++;
+        for (int c = 0; c < 4; c++) tma_load_3d(sm + oQ + c * 16384, tm, land, 64 * c, h0, sg.tok0);
+    }
+    __syncwarp();
     const RowOf o(p, w, sg, r);
-    const bool live = o.live;
-    const int tok = sg.tok0 + (live ? o.ti : 0);
+    const int tok = sg.tok0 + (o.live ? o.ti : 0);
     const uint4 *src = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + (long long)tok * p.q_ts +
-                                                       (live ? o.h : 0) * p.q_hs);
-#pragma unroll
-    for (int c = 0; c < 32; c++) cp16(smem_u32(sm) + oQ + (c >> 3) * 16384 + sw128(r, c & 7), src + 32 + c, live);
+                                                       (o.live ? o.h : 0) * p.q_hs + kDL);
+    const float4 *tab = reinterpret_cast<const float4 *>(w.tab + (size_t)tok * 32);
     tc_fence_after();
     uint32_t x[32], lo[32];
-    auto load = [&](int c, uint32_t(&y)[32]) {
-#pragma unroll
-        for (int u = 0; u < 8; u++) {
-            const uint4 v = live ? __ldg(src + 8 * c + u) : make_uint4(0, 0, 0, 0);
-            y[4 * u] = v.x;
-            y[4 * u + 1] = v.y;
-            y[4 * u + 2] = v.z;
-            y[4 * u + 3] = v.w;
-        }
-    };
-#pragma unroll
-    for (int c = 0; c < 4; c += 2) {
-        load(c, x);
-        load(c + 1, lo);
-        tmem_st32u(trow + kColQ + 32 * c, x);
-        tmem_st32u(trow + kColQ + 32 * c + 32, lo);
-    }
-    const float4 *tab = reinterpret_cast<const float4 *>(w.tab + (size_t)tok * 32);
 #pragma unroll
     for (int u = 0; u < 8; u++) {
-        const uint4 v = live ? __ldg(src + kDL / 8 + u) : make_uint4(0, 0, 0, 0);
+        const uint4 v = o.live ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
         const float4 c0 = __ldg(tab + 2 * u), c1 = __ldg(tab + 2 * u + 1);
         const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
         const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
@@ -173,21 +164,43 @@ __device__ __forceinline__ void load_q(const Paged &p, const PagedPlan &w, const
     }
     tmem_st32u(trow + kColR, x);
     tmem_st32u(trow + kColR + 32, lo);
+    if (!warp_all(mbar_wait(land, 0, abort_flag, wlim))) return false;  // (its even phase)
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(sm + oQ + c * 16384 + sw128(r, u));
+            x[4 * u] = v.x;
+            x[4 * u + 1] = v.y;
+            x[4 * u + 2] = v.z;
+            x[4 * u + 3] = v.w;
+        }
+        tmem_st32u(trow + kColQ + 32 * c, x);
+    }
     tmem_wait_st();
     tc_fence_before();
-    cp_wait_all();
-    fence_proxy_async_smem();
-}
-__device__ __forceinline__ void prefetch_q(const Paged &p, const PagedPlan &w, const Seg &sg, int r) {
-    const RowOf o(p, w, sg, r);
-    if (!o.live) return;
-    const __nv_bfloat16 *row = (const __nv_bfloat16 *)p.q + (long long)(sg.tok0 + o.ti) * p.q_ts + o.h * p.q_hs;
-    for (int i = 0; i < 9; i++) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64 * i));
+    fence_proxy_async_smem();  // the reads come before the next copies' writes
+    __syncwarp();
+    if (lane == 0) {
+        mbar_arrive(read);
+        mbar_arrive(ready);
+    }
+    bool ok = true;
+    if (wr == 0 && lane == 0) {
+        ok = mbar_wait(read, k & 1, abort_flag, wlim);
+        if (ok) {
+            mbar_arrive_expect_tx(land, 4 * bytes);
+            armed++;
+            for (int c = 0; c < 4; c++) tma_load_3d(sm + oQ + c * 16384, tm, land, 64 * (4 + c), h0, sg.tok0);
+        }
+    }
+    return warp_all(ok);
 }
 
 template <int KIND>
 __global__ void __launch_bounds__(threads_of(KIND), 1)
-    k_paged_tc(const __grid_constant__ CUtensorMap tm_k4, const __grid_constant__ CUtensorMap tm_k1, const Paged p, const PagedPlan w) {
+    k_paged_tc(const __grid_constant__ CUtensorMap tm_k4, const __grid_constant__ CUtensorMap tm_k1,
+               const __grid_constant__ CUtensorMap tm_q, const Paged p, const PagedPlan w) {
     constexpr int kWarpM = issuer_warp(KIND), kThreads = threads_of(KIND);
     constexpr int kFull = KIND == DSPARK_CACHE_BF16 ? 2 : 4;  // arrivals for a part of a stage
     extern __shared__ __align__(1024) uint8_t sm[];  // swizzle atoms: no room for slack
@@ -195,7 +208,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + 4;
     uint64_t *sfull = kempty + 4, *sfree = sfull + 1, *pready = sfull + 2, *pvdone = sfull + 3;
     uint64_t *qready = sfull + 4, *qfree = sfull + 5, *ofree = sfull + 6, *drain = sfull + 7;
-    uint64_t *xbar = sfull + 9, *lbar = xbar + 8;
+    uint64_t *qland = sfull + 9, *qread = sfull + 10, *xbar = sfull + 11, *lbar = xbar + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lbar + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(lbar + 4) + 1;
     // [4][4]: 16 keys' validity each, of step g at g % 4 (a stage's first part is
@@ -215,6 +228,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         mbar_init(pready, kSoft);
         mbar_init(pvdone, 1);
         mbar_init(qready, 4);
+        mbar_init(qland, 1);
+        mbar_init(qread, 4);
         mbar_init(qfree, 1);
         mbar_init(ofree, kSoft);
         mbar_init(&drain[0], 1);
@@ -237,7 +252,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     SegCursor cur;
     cur.begin(w);
     Seg sg;
-    uint32_t issued = 0;  // the TMA loader's parts of steps
+    uint32_t issued = 0, q_issued = 0;  // the loaders' parts of steps; copies of Q
+    const uint32_t q_bytes = 128u * min(p.n_h, 128) * w.tpt;  // of a slice
 
     if (KIND == DSPARK_CACHE_BF16 && warp == kWarpKeys) {
         // ------------------------------------------------- bf16 keys -> stages
@@ -326,15 +342,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         bool ok = true;
         for (; ok && cur.next(p, w, sg); k++) {
             if (gp == 0) {
-                const int r = wr * 32 + lane;
-                if (k > 0) {
-                    prefetch_q(p, w, sg, r);
-                    ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
-                }
+                if (k > 0) ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
                 if (!ok) break;
-                load_q(p, w, sg, sm, tmem + ((uint32_t)(wr * 32) << 16), r);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(qready);
+                ok = load_q(p, w, sg, &tm_q, sm, tmem, wr, q_bytes, qland, qread, qready, k, q_issued, abort_flag, wlim);
+                if (!ok) break;
             }
             for (int t = sg.s0; ok && t < sg.s1; t++, g++) {
                 if ((int)(g & 1) != gp) continue;
@@ -348,19 +359,25 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0) & 0xffffu;
                 const uint8_t *cache = (const uint8_t *)p.cache;
                 const long long off = slot >= 0 ? slot * (long long)p.row_bytes : -1;
-                // lane: rows 8 rb + lane / 4, 16 codes of each slice
+                // lane: rows 8 rb + lane / 4, 16 codes of each slice; x[.][0 .. 3] of the
+                // other half, x[.][4 .. 7] of the own
                 uint4 x[2][8];
-                float4 sc[2];
+                float2 sc[2][2];
 #pragma unroll
                 for (int rb = 0; rb < 2; rb++) {
                     const long long o = __shfl_sync(0xffffffffu, off, 8 * rb + (lane >> 2));
                     const uint8_t *row = cache + (o >= 0 ? o : 0);
-                    sc[rb] = o >= 0 ? __ldg(reinterpret_cast<const float4 *>(row + kDL + 2 * kDR))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int s = 0; s < 8; s++)
-                        x[rb][s] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * s + 16 * (lane & 3)))
-                                          : make_uint4(0, 0, 0, 0);
+                    for (int part = 0; part < 2; part++) {
+                        const int up = half ^ part ^ 1;
+                        sc[rb][part] = o >= 0 ? __ldg(reinterpret_cast<const float2 *>(row + kDL + 2 * kDR) + up)
+                                              : make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int n = 0; n < 4; n++)
+                            x[rb][4 * part + n] =
+                                o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(row + 256 * up + 64 * n + 16 * (lane & 3)))
+                                       : make_uint4(0, 0, 0, 0);
+                    }
                 }
 #pragma unroll
                 for (int part = 0; part < 2; part++) {
@@ -377,16 +394,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                                  cache + (o >= 0 ? o + kDL + ch * 16 : 0), o >= 0);
                         }
                     }
-                    const bool upper = (half ^ part ^ 1) != 0;  // slices 4 - 7 or 0 - 3
 #pragma unroll
                     for (int rb = 0; rb < 2; rb++) {
                         uint8_t *dst = sm + gp * kStage + (part ? oPartB + (2 * wr + rb) * kGroupB : (2 * wr + rb) * kGroupA);
 #pragma unroll
                         for (int n = 0; n < 4; n++) {
-                            const float f = upper ? (n < 2 ? sc[rb].z : sc[rb].w) : (n < 2 ? sc[rb].x : sc[rb].y);
-                            const uint4 a = x[rb][n], b = x[rb][4 + n];
-                            const uint4 v = make_uint4(upper ? b.x : a.x, upper ? b.y : a.y, upper ? b.z : a.z,
-                                                       upper ? b.w : a.w);
+                            const float f = n < 2 ? sc[rb][part].x : sc[rb][part].y;
+                            const uint4 v = x[rb][4 * part + n];
                             *reinterpret_cast<uint4 *>(dst + n * 1024 + sw128(lane >> 2, 2 * (lane & 3))) =
                                 make_uint4(fp8x2_bf16(v.x, f), fp8x2_bf16(v.x >> 16, f), fp8x2_bf16(v.y, f),
                                            fp8x2_bf16(v.y >> 16, f));
@@ -405,18 +419,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         cp_wait_all();
     } else if (KIND == DSPARK_CACHE_BF16 && warp >= kWarpQ && warp < kWarpKeys) {
         // -------------------------------------- Q -> shared and tensor memory
-        const int r = (warp - kWarpQ) * 32 + lane;
         uint32_t k = 0;  // segments
         bool ok = true;
         for (; ok && cur.next(p, w, sg); k++) {
-            prefetch_q(p, w, sg, r);
             if (k > 0) ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
             if (!ok) break;
-            load_q(p, w, sg, sm, tmem + ((uint32_t)((warp - kWarpQ) * 32) << 16), r);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(qready);
+            ok = load_q(p, w, sg, &tm_q, sm, tmem, warp - kWarpQ, q_bytes, qland, qread, qready, k, q_issued, abort_flag, wlim);
         }
-        cp_wait_all();
     } else if (warp == kWarpM) {
         // ------------------------------------------------------ S = Q K^T
         if (lane == 0) {
@@ -441,7 +450,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             for (; ok && cur.next(p, w, sg); k++)
                 for (int t = sg.s0; t < sg.s1; t++, g++) {
                     const int st = g & 1;
-                    if (t == sg.s0 && !wait(qready, k & 1)) break;
+                    // (Q in tensor memory, then in shared memory: its barrier's odd phase)
+                    if (t == sg.s0 && (!wait(qready, k & 1) || !wait(qland, 1))) break;
                     if (g > 0 && !wait(sfree, (g - 1) & 1)) break;
                     if (!wait(&kfull[2 * st], (g >> 1) & 1)) break;
                     tc_fence_after();
@@ -607,27 +617,31 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 dst = (uint8_t *)((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs + col0);
                 if (half == 0 && hf == 0) p.lse[(size_t)tok * p.n_h + h] = lse2 * kLn2;
             }
+            const float f = lt > 0.f ? inv : 0.f;
+            const bool wide = ((uintptr_t)dst & 31) == 0;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
                 float o[32];
                 tmem_ld32(trow + kColO + 128 * hf + c, o);
                 tmem_wait_ld();
+                // (a row that sees no key may hold what was there before)
+#pragma unroll
+                for (int i = 0; i < 32; i++) o[i] = lt > 0.f ? o[i] * f : 0.f;
                 if (pdst && live) {
 #pragma unroll
-                    for (int u = 0; u < 8; u++)
-                        *reinterpret_cast<float4 *>(pdst + c + 4 * u) =
-                            lt > 0.f ? make_float4(o[4 * u] * inv, o[4 * u + 1] * inv, o[4 * u + 2] * inv, o[4 * u + 3] * inv)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int u = 0; u < 4; u++) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) x[i] = __float_as_uint(o[8 * u + i]);
+                        st_global_32B(pdst + c + 8 * u, x, true);
+                    }
                 } else if (dst) {
 #pragma unroll
-                    for (int u = 0; u < 4; u++) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (lt > 0.f)
-                            x = make_uint4(pack_bf16x2(o[8 * u] * inv, o[8 * u + 1] * inv),
-                                           pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
-                                           pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
-                                           pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
-                        *reinterpret_cast<uint4 *>(dst + 2 * c + 16 * u) = x;
+                    for (int u = 0; u < 2; u++) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) x[i] = pack_bf16x2(o[16 * u + 2 * i], o[16 * u + 2 * i + 1]);
+                        st_global_32B(dst + 2 * c + 32 * u, x, wide);
                     }
                 }
             }
@@ -677,6 +691,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         if (KIND == DSPARK_CACHE_BF16 && warp == kWarpKeys)
             for (uint32_t n = issued > 4 ? issued - 4 : 0; n < issued; n++)  // part n % 2 of step n / 2
                 mbar_wait(&kfull[n & 3], (n >> 2) & 1, &never);
+        if (warp == kWarpQ && q_issued) mbar_wait(qland, (q_issued - 1) & 1, &never);
         if (warp >= kWarpM) {
             mma_commit(&drain[warp - kWarpM]);
             mbar_wait(&drain[warp - kWarpM], 0, &never);
@@ -701,13 +716,12 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
     const int units = w.head->n_split * 128;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const int r = w.split[u >> 7], row = u & 127;
-        const long long t0 = w.start[r], t1 = w.start[r + 1];
-        const int4 tl = w.tiles[r];
-        const SeqView v = seq_view(p, tl.x);
+        const PagedTile tl = w.tiles[r];
+        const long long t0 = tl.start, t1 = t0 + tl.steps;
         const int p0 = (int)(t0 / per), n = (int)((t1 - 1) / per) - p0 + 1;
         const int grp = threadIdx.x >> 7, c = threadIdx.x & 127;
-        const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.z * 128 + row - ti * p.n_h;
-        if (ti >= min(w.tpt, v.q_len - tl.y) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
+        const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.hc * 128 + row - ti * p.n_h;
+        if (ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
         // part k: pair p0 + k, its slot 1 for the tile's beginning, 0 after it
         __syncthreads();
         if (threadIdx.x < n) wt[threadIdx.x] = w.part_lse[(2 * (p0 + threadIdx.x) + (threadIdx.x == 0)) * 128 + row];
@@ -738,7 +752,7 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
                 acc.z += sum[k][c].z;
                 acc.w += sum[k][c].w;
             }
-            const int tok = v.q0 + tl.y + ti;
+            const int tok = tl.q0 + tl.i0 + ti;
             *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs + 4 * c) =
                 make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
             if (c == 0) p.lse[(size_t)tok * p.n_h + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
@@ -747,11 +761,11 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
 }
 
 template <int KIND>
-cudaError_t launch_t(const CUtensorMap &m4, const CUtensorMap &m1, const Paged &p, const PagedPlan &w, cudaStream_t st) {
+cudaError_t launch_t(const CUtensorMap &m4, const CUtensorMap &m1, const CUtensorMap &mq, const Paged &p, const PagedPlan &w, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(k_paged_tc<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     count_launch();
-    return launch_pdl(k_paged_tc<KIND>, dim3(2 * kPairs), dim3(threads_of(KIND)), kSmem, st, m4, m1, p, w);
+    return launch_pdl(k_paged_tc<KIND>, dim3(2 * kPairs), dim3(threads_of(KIND)), kSmem, st, m4, m1, mq, p, w);
 }
 
 }  // namespace
@@ -764,8 +778,14 @@ cudaError_t launch_paged_tc(const Paged &p, const PagedPlan &w, cudaStream_t st)
     if (p.kind == DSPARK_CACHE_BF16 &&
         (!make_map_nd(&m4, p.cache, 3, dims, strides, b4) || !make_map_nd(&m1, p.cache, 3, dims, strides, b1)))
         return cudaErrorInvalidValue;
-    cudaError_t e = p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(m4, m1, p, w, st)
-                                                : launch_t<DSPARK_CACHE_FP8>(m4, m1, p, w, st);
+    // queries: 64 columns, heads, tokens (the stride of an extent of one is not used)
+    CUtensorMap mq{};
+    const uint64_t qd[3] = {kDL + kDR, (uint64_t)p.n_h, (uint64_t)p.T};
+    const uint64_t qs[2] = {p.n_h > 1 ? 2 * (uint64_t)p.q_hs : 2 * (kDL + kDR), p.T > 1 ? 2 * (uint64_t)p.q_ts : 2 * (kDL + kDR)};
+    const uint32_t qb[3] = {64, (uint32_t)std::min(p.n_h, 128), (uint32_t)w.tpt};
+    if (!make_map_nd(&mq, p.q, 3, qd, qs, qb)) return cudaErrorInvalidValue;
+    cudaError_t e = p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(m4, m1, mq, p, w, st)
+                                                : launch_t<DSPARK_CACHE_FP8>(m4, m1, mq, p, w, st);
     if (e != cudaSuccess) return e;
     count_launch();
     return launch_pdl(k_paged_join, dim3(296), dim3(512), 0, st, p, w);

@@ -706,57 +706,106 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
 }
 
-// Joins the parts of the tiles that pairs shared, a row to a CTA at a time; four
-// groups of 128 threads take every fourth part, four columns to a thread.
+// Joins the parts of the tiles that pairs shared: part k of a tile is pair
+// p0 + k's, in its slot 1 for the tile's beginning, 0 after it.
+__device__ __forceinline__ size_t part_row(int p0, int k, int row) {
+    return (size_t)(2 * (p0 + k) + (k == 0)) * 128 + row;
+}
+// Tiles of up to kFew parts go a row to a warp (16 columns to a lane), others a
+// row to a CTA: four groups of 128 threads take every fourth part, four columns
+// to a thread.
+constexpr int kFew = 8;
 __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPlan w) {
     __shared__ float wt[kPairs + 1];
     __shared__ float4 sum[3][128];
     pdl_wait();
     const long long per = w.head->per;
-    const int units = w.head->n_split * 128;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        const int r = w.split[u >> 7], row = u & 127;
-        const PagedTile tl = w.tiles[r];
-        const long long t0 = tl.start, t1 = t0 + tl.steps;
-        const int p0 = (int)(t0 / per), n = (int)((t1 - 1) / per) - p0 + 1;
-        const int grp = threadIdx.x >> 7, c = threadIdx.x & 127;
-        const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.hc * 128 + row - ti * p.n_h;
-        if (ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
-        // part k: pair p0 + k, its slot 1 for the tile's beginning, 0 after it
-        __syncthreads();
-        if (threadIdx.x < n) wt[threadIdx.x] = w.part_lse[(2 * (p0 + threadIdx.x) + (threadIdx.x == 0)) * 128 + row];
-        __syncthreads();
-        float m = -INFINITY, l = 0.f;
-        for (int k = 0; k < n; k++) m = wt[k] != wt[k] || m != m ? NAN : fmaxf(m, wt[k]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (m != -INFINITY) {
-            for (int k = 0; k < n; k++) l += exp2f(wt[k] - m);
+    const int n_split = w.head->n_split, lane = threadIdx.x & 31;
+    const int grp = threadIdx.x >> 7, c = threadIdx.x & 127;
+    bool many = false;
+    for (int t = 0; t < n_split; t++) {
+        const PagedTile &tl = w.tiles[w.split[t]];
+        many |= (int)((tl.start + tl.steps - 1) / per - tl.start / per) + 1 > kFew;
+    }
+    if (many) {
+        for (int u = blockIdx.x; u < n_split * 128; u += gridDim.x) {
+            const PagedTile tl = w.tiles[w.split[u >> 7]];
+            const int row = u & 127, p0 = (int)(tl.start / per), n = (int)((tl.start + tl.steps - 1) / per) - p0 + 1;
+            const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.hc * 128 + row - ti * p.n_h;
+            if (n <= kFew || ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
+            __syncthreads();
+            if (threadIdx.x < n) wt[threadIdx.x] = w.part_lse[part_row(p0, threadIdx.x, row)];
+            __syncthreads();
+            float m = -INFINITY, l = 0.f;
+            for (int k = 0; k < n; k++) m = wt[k] != wt[k] || m != m ? NAN : fmaxf(m, wt[k]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m != -INFINITY) {
+                for (int k = 0; k < n; k++) l += exp2f(wt[k] - m);
 #pragma unroll 8
-            for (int k = grp; k < n; k += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(
-                                           w.part_o + ((size_t)(2 * (p0 + k) + (k == 0)) * 128 + row) * kDL) + c);
-                const float f = exp2f(wt[k] - m) / l;
-                acc.x = fmaf(f, x.x, acc.x);
-                acc.y = fmaf(f, x.y, acc.y);
-                acc.z = fmaf(f, x.z, acc.z);
-                acc.w = fmaf(f, x.w, acc.w);
+                for (int k = grp; k < n; k += 4) {
+                    const float4 x = __ldg(reinterpret_cast<const float4 *>(w.part_o + part_row(p0, k, row) * kDL) + c);
+                    const float f = exp2f(wt[k] - m) / l;
+                    acc.x = fmaf(f, x.x, acc.x);
+                    acc.y = fmaf(f, x.y, acc.y);
+                    acc.z = fmaf(f, x.z, acc.z);
+                    acc.w = fmaf(f, x.w, acc.w);
+                }
             }
-        }
-        if (grp) sum[grp - 1][c] = acc;
-        __syncthreads();
-        if (grp == 0) {
+            if (grp) sum[grp - 1][c] = acc;
+            __syncthreads();
+            if (grp == 0) {
 #pragma unroll
-            for (int k = 0; k < 3; k++) {
-                acc.x += sum[k][c].x;
-                acc.y += sum[k][c].y;
-                acc.z += sum[k][c].z;
-                acc.w += sum[k][c].w;
+                for (int k = 0; k < 3; k++) {
+                    acc.x += sum[k][c].x;
+                    acc.y += sum[k][c].y;
+                    acc.z += sum[k][c].z;
+                    acc.w += sum[k][c].w;
+                }
+                const int tok = tl.q0 + tl.i0 + ti;
+                *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs + 4 * c) =
+                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                if (c == 0) p.lse[(size_t)tok * p.n_h + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
             }
-            const int tok = tl.q0 + tl.i0 + ti;
-            *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs + 4 * c) =
-                make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            if (c == 0) p.lse[(size_t)tok * p.n_h + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
         }
+    }
+    for (int u = blockIdx.x * 16 + (threadIdx.x >> 5); u < n_split * 128; u += gridDim.x * 16) {
+        const PagedTile tl = w.tiles[w.split[u >> 7]];
+        const int row = u & 127, p0 = (int)(tl.start / per), n = (int)((tl.start + tl.steps - 1) / per) - p0 + 1;
+        const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.hc * 128 + row - ti * p.n_h;
+        if (n > kFew || ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
+        const float mine = lane < n ? w.part_lse[part_row(p0, lane, row)] : -INFINITY;
+        const bool nan = __any_sync(0xffffffffu, mine != mine);
+        float m = mine;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = nan ? NAN : __shfl_sync(0xffffffffu, m, 0);
+        float f = m == -INFINITY || lane >= n ? 0.f : exp2f(mine - m), l = f;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        l = __shfl_sync(0xffffffffu, l, 0);
+        f = l != 0.f ? f / l : 0.f;
+        float4 acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int k = 0; k < n; k++) {
+            const float g = __shfl_sync(0xffffffffu, f, k);
+            const float4 *src = reinterpret_cast<const float4 *>(w.part_o + part_row(p0, k, row) * kDL);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float4 x = __ldg(src + lane + 32 * i);
+                acc[i].x = fmaf(g, x.x, acc[i].x);
+                acc[i].y = fmaf(g, x.y, acc[i].y);
+                acc[i].z = fmaf(g, x.z, acc[i].z);
+                acc[i].w = fmaf(g, x.w, acc[i].w);
+            }
+        }
+        const int tok = tl.q0 + tl.i0 + ti;
+        uint2 *dst = reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            dst[lane + 32 * i] = make_uint2(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i].z, acc[i].w));
+        if (lane == 0) p.lse[(size_t)tok * p.n_h + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
 }
 

@@ -499,8 +499,7 @@ def latent_cache_read(cache, slots, d_l=512, d_r=64, dtype=torch.bfloat16, strea
     kind = _cache_kind(cache, d_l, d_r)
     dev, T = cache.device, slots.numel()
     _same("slots", slots, (T,), torch.int64, dev)
-    c = torch.empty((T, d_l), dtype=dtype, device=dev)
-    kr = torch.empty((T, d_r), dtype=dtype, device=dev)
+    c, kr = cache.new_empty((T, d_l), dtype=dtype), cache.new_empty((T, d_r), dtype=dtype)
     prob = LatentCache(T, d_l, d_r, kind, cache.shape[0], cache.shape[1], dtype_code(dtype), 0)
     _call("dspark_latent_cache_read", dev, stream, ctypes.byref(prob), _at(cache), _at(slots), _at(c), _at(kr))
     return c, kr

@@ -1,6 +1,13 @@
 // The paged latent cache: rows written (RMS norm, rope turn, rounding) and read
 // back as the values that they stand for. One warp per token; both are bound by
 // the bytes of the rows at many tokens and by one launch's latency at few.
+//
+// A written value is the nearest of the exact x * rsqrt(mean x^2 + eps) * w (to
+// 2^-40 of it), so a value that ends in 8 bits has no second rounding on its way.
+// That takes more than fp32; fp64 throughout was bound by its conversions, so bf16
+// inputs use pairs of fp32: squares and x * w are exact in fp32, the sum keeps its
+// rounding errors, and the product with the pair of the root is formed with its
+// remainder.
 #include <cmath>
 
 #include "dspark_latent.cuh"
@@ -57,14 +64,23 @@ __device__ __forceinline__ float to_f_sticky(double x) {
     return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// Least e >= -117 with amax <= 448 * 2^e (448 = 0.875 * 2^9); 0 for amax = 0.
-__device__ __forceinline__ int fp8_exp(double amax) {
-    if (amax == 0.0) return 0;
-    int x;
-    const double m = frexp(amax, &x);
-    return max(m <= 0.875 ? x - 9 : x - 8, -117);
+// The same of p + e, |e| at most half a unit of p.
+__device__ __forceinline__ float to_f_sticky(float p, float e) {
+    if (e == 0.f || !(fabsf(p) <= 3.4028235e38f)) return p;
+    const uint32_t b = __float_as_uint(p);
+    // towards zero where the remainder has the other sign
+    return __uint_as_float((((b ^ __float_as_uint(e)) >> 31) ? b - 1 : b) | 1u);
 }
-__device__ __forceinline__ double pow2d(int e) { return __longlong_as_double((long long)(e + 1023) << 52); }
+
+// Least e >= -117 with amax <= 448 * 2^e (448 = 0.875 * 2^9); 0 for amax = 0.
+// (amax: a value or its sticky form; 0.875 * 2^x is exact in either)
+__device__ __forceinline__ int fp8_exp(float amax) {
+    if (amax == 0.f) return 0;
+    int x;
+    const float m = frexpf(amax, &x);
+    return max(m <= 0.875f ? x - 9 : x - 8, -117);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 __device__ __forceinline__ uint32_t e4m3_code(float x) {
     // a value that is not finite is kept as NaN, not saturated
@@ -86,15 +102,25 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache
     if (slot < 0 || slot >= (int64_t)p.n_pages * p.page_size) return;  // the whole warp
     uint8_t *row = cache + (size_t)slot * row_bytes;
     // lane l holds values 8 l .. 8 l + 7 and, above 256 wide, 256 + 8 l ..
+    constexpr bool kPairs = sizeof(T) == 2;  // squares and x * w are exact in fp32
     float x[2][8];
     double ss = 0.0;
+    float s1 = 0.f, s2 = 0.f;  // sum of squares and its rounding errors
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const int d = 256 * i + 8 * lane;
         if (d < p.d_l) {
             load8(c + (size_t)t * p.d_l + d, x[i]);
 #pragma unroll
-            for (int k = 0; k < 8; k++) ss += (double)x[i][k] * (double)x[i][k];
+            for (int k = 0; k < 8; k++) {
+                if constexpr (kPairs) {
+                    const float q = x[i][k] * x[i][k], n = s1 + q, v = n - s1;
+                    s2 += (s1 - (n - v)) + (q - v);
+                    s1 = n;
+                } else {
+                    ss += (double)x[i][k] * (double)x[i][k];
+                }
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < 8; k++) x[i][k] = 0.f;
@@ -102,56 +128,69 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache
     }
     double rn = 1.0;
     if (w) {
+        // (squares that leave fp32's range at either end: formed again in fp64)
+        if (kPairs && s1 >= 1e-20f && s1 <= 3.4028235e38f) {
+            ss = (double)s1 + (double)s2;
+        } else if (kPairs) {
+            for (int i = 0; i < 2; i++)
+                for (int k = 0; k < 8; k++) ss += (double)x[i][k] * (double)x[i][k];
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         rn = 1.0 / sqrt(ss / p.d_l + eps);
     }
+    const float rh = (float)rn, rl = fabsf(rh) <= 3.4028235e38f ? (float)(rn - (double)rh) : 0.f;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const int d = 256 * i + 8 * lane;
-        double y[8];
+        float z[8];  // sticky values; for fp32 rows, the nearest
         if (w && d < p.d_l) {
             float wv[8];
             load8(w + d, wv);
 #pragma unroll
-            for (int k = 0; k < 8; k++) y[k] = (double)x[i][k] * rn * (double)wv[k];
+            for (int k = 0; k < 8; k++) {
+                const float u = x[i][k] * wv[k], q = u * rh;
+                // (far from both ends of fp32's range, where the pair is exact)
+                if (kPairs && fabsf(q) <= 1e37f && (fabsf(q) >= 1e-28f || q == 0.f) && fabsf(u) >= 1e-28f &&
+                    fabsf(u) <= 1e37f) {
+                    const float e = fmaf(u, rl, fmaf(u, rh, -q)), sum = q + e, rest = (q - sum) + e;
+                    z[k] = KIND == DSPARK_CACHE_F32 ? sum : to_f_sticky(sum, rest);
+                } else {
+                    const double y = (double)x[i][k] * rn * (double)wv[k];
+                    z[k] = KIND == DSPARK_CACHE_F32 ? (float)y : to_f_sticky(y);
+                }
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; k++) y[k] = (double)x[i][k];
+            for (int k = 0; k < 8; k++) z[k] = x[i][k];
         }
         if constexpr (KIND == DSPARK_CACHE_FP8) {
             // a group of 128 values is 16 lanes
-            double am = 0.0;
+            float am = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                const double v = fabs(y[k]);
-                if (v <= 1.7976931348623157e308) am = fmax(am, v);
+                const float v = fabsf(z[k]);
+                if (v <= 3.4028235e38f) am = fmaxf(am, v);
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) am = fmax(am, __shfl_xor_sync(0xffffffffu, am, o));
+            for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
             const int e = fp8_exp(am);
-            const double inv = pow2d(-e);
+            const float inv = pow2f(-e);
             uint32_t lo = 0, hi = 0;
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-                lo |= e4m3_code(to_f_sticky(y[k] * inv)) << (8 * k);
-                hi |= e4m3_code(to_f_sticky(y[4 + k] * inv)) << (8 * k);
+                lo |= e4m3_code(z[k] * inv) << (8 * k);
+                hi |= e4m3_code(z[4 + k] * inv) << (8 * k);
             }
             if (d < p.d_l) {
                 *reinterpret_cast<uint2 *>(row + d) = make_uint2(lo, hi);
-                if ((lane & 15) == 0)
-                    *reinterpret_cast<float *>(row + p.d_l + 2 * p.d_r + 4 * (d >> 7)) = (float)pow2d(e);
+                if ((lane & 15) == 0) *reinterpret_cast<float *>(row + p.d_l + 2 * p.d_r + 4 * (d >> 7)) = pow2f(e);
             }
-        } else {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; k++) f[k] = KIND == DSPARK_CACHE_BF16 ? to_f_sticky(y[k]) : (float)y[k];
-            if (d < p.d_l) {
-                if constexpr (KIND == DSPARK_CACHE_BF16)
-                    store8(reinterpret_cast<__nv_bfloat16 *>(row) + d, f);
-                else
-                    store8(reinterpret_cast<float *>(row) + d, f);
-            }
+        } else if (d < p.d_l) {
+            if constexpr (KIND == DSPARK_CACHE_BF16)
+                store8(reinterpret_cast<__nv_bfloat16 *>(row) + d, z);
+            else
+                store8(reinterpret_cast<float *>(row) + d, z);
         }
     }
     // the rope key: lane l turns pairs l, l + 32
@@ -172,54 +211,94 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache
     }
 }
 
-template <typename T, int KIND>
+// NT tokens to a warp: their slots together, then all rows' loads, so that many
+// tokens wait for two latencies once (32768 8-bit rows: 18 us with one token to a
+// warp). Few tokens keep one to a warp, for as many SMs as there are.
+template <typename T, int KIND, int NT>
 __global__ void __launch_bounds__(kWarps * 32) k_cache_read(dspark_latent_cache p, const uint8_t *__restrict__ cache,
                                                             size_t row_bytes, const int64_t *__restrict__ slots,
                                                             T *__restrict__ c_out, T *__restrict__ kr_out) {
     const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= p.T) return;
-    const int64_t slot = slots[t];
-    const bool ok = slot >= 0 && slot < (int64_t)p.n_pages * p.page_size;
-    const uint8_t *row = cache + (size_t)(ok ? slot : 0) * row_bytes;
+    const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * NT;
+    if (t0 >= p.T) return;
+    int64_t mine = -1;
+    if (lane < NT && t0 + lane < p.T) mine = slots[t0 + lane];
+    if (mine >= (int64_t)p.n_pages * p.page_size) mine = -1;
+    const uint8_t *row[NT];
+    bool ok[NT];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        const int64_t slot = __shfl_sync(0xffffffffu, mine, n);
+        ok[n] = slot >= 0;
+        row[n] = cache + (size_t)(ok[n] ? slot : 0) * row_bytes;
+    }
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const int d = 256 * i + 8 * lane;
         if (d >= p.d_l) continue;
-        float v[8];
+        if constexpr (KIND == DSPARK_CACHE_FP8) {
+            uint2 w[NT];
+            float s[NT];
 #pragma unroll
-        for (int k = 0; k < 8; k++) v[k] = 0.f;
-        if (ok) {
-            if constexpr (KIND == DSPARK_CACHE_FP8) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(row + d);
-                const float s = *reinterpret_cast<const float *>(row + p.d_l + 2 * p.d_r + 4 * (d >> 7));
+            for (int n = 0; n < NT; n++) {
+                w[n] = ok[n] ? *reinterpret_cast<const uint2 *>(row[n] + d) : make_uint2(0, 0);
+                s[n] = ok[n] ? *reinterpret_cast<const float *>(row[n] + p.d_l + 2 * p.d_r + 4 * (d >> 7)) : 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                if (t0 + n >= p.T) continue;
+                float v[8];
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     __nv_fp8_e4m3 q;
-                    q.__x = (uint8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
-                    v[k] = (float)q * s;
+                    q.__x = (uint8_t)((k < 4 ? w[n].x : w[n].y) >> (8 * (k & 3)));
+                    v[k] = (float)q * s[n];
                 }
-            } else if constexpr (KIND == DSPARK_CACHE_BF16) {
-                load8(reinterpret_cast<const __nv_bfloat16 *>(row) + d, v);
-            } else {
-                load8(reinterpret_cast<const float *>(row) + d, v);
+                store8(c_out + (size_t)(t0 + n) * p.d_l + d, v);
             }
+        } else {
+            float v[NT][8];
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                if (ok[n]) {
+                    if constexpr (KIND == DSPARK_CACHE_BF16)
+                        load8(reinterpret_cast<const __nv_bfloat16 *>(row[n]) + d, v[n]);
+                    else
+                        load8(reinterpret_cast<const float *>(row[n]) + d, v[n]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; k++) v[n][k] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+                if (t0 + n < p.T) store8(c_out + (size_t)(t0 + n) * p.d_l + d, v[n]);
         }
-        store8(c_out + (size_t)t * p.d_l + d, v);
     }
     if (!kr_out) return;
-    for (int d = 8 * lane; d < p.d_r; d += 256) {
+    // the rope keys: 8 values to a lane, token by token
+    const int per = p.d_r / 8;
+    for (int e = lane; e < NT * per; e += 32) {
+        const int n = e / per, d = 8 * (e % per);
+        if (t0 + n >= p.T) continue;
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; k++) v[k] = 0.f;
-        if (ok) {
+        bool good = ok[0];
+        const uint8_t *r = row[0];
+#pragma unroll
+        for (int m = 1; m < NT; m++)
+            if (n == m) {
+                good = ok[m];
+                r = row[m];
+            }
+        if (good) {
             if constexpr (KIND == DSPARK_CACHE_F32)
-                load8(reinterpret_cast<const float *>(row) + p.d_l + d, v);
+                load8(reinterpret_cast<const float *>(r) + p.d_l + d, v);
             else
-                load8(reinterpret_cast<const __nv_bfloat16 *>(row + (KIND == DSPARK_CACHE_FP8 ? p.d_l : 2 * p.d_l)) + d,
-                      v);
+                load8(reinterpret_cast<const __nv_bfloat16 *>(r + (KIND == DSPARK_CACHE_FP8 ? p.d_l : 2 * p.d_l)) + d, v);
         }
-        store8(kr_out + (size_t)t * p.d_r + d, v);
+        store8(kr_out + (size_t)(t0 + n) * p.d_r + d, v);
     }
 }
 
@@ -251,11 +330,19 @@ cudaError_t launch_cache_write(const dspark_latent_cache &p, const void *c, cons
 cudaError_t launch_cache_read(const dspark_latent_cache &p, const void *cache, const int64_t *slots, void *c_out,
                               void *kr_out, cudaStream_t st) {
     if (p.T == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)((p.T + kWarps - 1) / kWarps);
+    // four tokens to a warp from where the SMs are full with one
+    const int nt = p.T >= 148 * 64 ? 4 : 1;
+    const unsigned grid = (unsigned)((p.T + kWarps * nt - 1) / (kWarps * nt));
     const size_t rb = cache_row_bytes(p.kind, p.d_l, p.d_r);
     count_launch();
-#define DSPARK_READ(T, K)                                                                                      \
-    k_cache_read<T, K><<<grid, kWarps * 32, 0, st>>>(p, (const uint8_t *)cache, rb, slots, (T *)c_out, (T *)kr_out)
+#define DSPARK_READ_N(T, K, NT)                                                                            \
+    k_cache_read<T, K, NT><<<grid, kWarps * 32, 0, st>>>(p, (const uint8_t *)cache, rb, slots, (T *)c_out, \
+                                                         (T *)kr_out)
+#define DSPARK_READ(T, K)                       \
+    do {                                        \
+        if (nt == 4) DSPARK_READ_N(T, K, 4);    \
+        else DSPARK_READ_N(T, K, 1);            \
+    } while (0)
     if (p.dtype == DSPARK_F32) {
         if (p.kind == DSPARK_CACHE_F32) DSPARK_READ(float, DSPARK_CACHE_F32);
         else if (p.kind == DSPARK_CACHE_BF16) DSPARK_READ(float, DSPARK_CACHE_BF16);
@@ -266,6 +353,7 @@ cudaError_t launch_cache_read(const dspark_latent_cache &p, const void *cache, c
         else DSPARK_READ(__nv_bfloat16, DSPARK_CACHE_FP8);
     }
 #undef DSPARK_READ
+#undef DSPARK_READ_N
     return cudaGetLastError();
 }
 

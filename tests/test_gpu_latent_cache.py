@@ -448,3 +448,34 @@ def test_a_serving_step(oracle_mod):
                          np.array([0, 5]), np.array([A + 5]), page, capi.LATENT_SCALE, True, 0, True)
     lp.check("verified o", vo, val["o"], err["o"])
     lp.check("verified lse", vl, val["lse"], err["lse"])
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_read_of_many_tokens(kind):
+    """From 9472 tokens on a warp reads several: every slot, repeated and padded ones too, in any order."""
+    cache, lat, rope = filled(81, kind, 40, 16, 256, 32)
+    g = torch.Generator().manual_seed(82)
+    slots = torch.randint(-3, 40 * 16 + 3, (9473,), generator=g)
+    c, kr = capi.latent_cache_read(cache, slots.cuda(), 256, 32, dtype=torch.float32)
+    ok = ((slots >= 0) & (slots < 640)).numpy()
+    at = slots.numpy()[ok]
+    assert np.array_equal(c.cpu().double().numpy()[ok], lat[at]) and np.array_equal(kr.cpu().double().numpy()[ok], rope[at])
+    assert torch.count_nonzero(c.cpu()[~ok]) == 0 and torch.count_nonzero(kr.cpu()[~ok]) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("size", [1e-18, 1e-30, 1e17, 1e30])
+def test_write_far_from_one(kind, size):
+    """Rows whose squares or products leave the middle of fp32's range: the same nearest values."""
+    g = torch.Generator().manual_seed(83)
+    c = (torch.randn(40, 512, generator=g) * size).to(torch.bfloat16)
+    w = (torch.randn(512, generator=g) * 3).to(torch.bfloat16)
+    cache = capi.latent_cache(3, 16, kind=KINDS[kind])
+    slots = torch.arange(40).cuda()
+    z = torch.zeros(40, 64, dtype=torch.bfloat16)
+    capi.latent_cache_write(cache, c.cuda(), z.cuda(), torch.zeros(40, dtype=torch.int32).cuda(), slots,
+                            norm_weight=w.cuda(), eps=1e-70)
+    got, _ = capi.latent_cache_read(cache, slots, dtype=torch.float32)
+    y = ol.norm_rows(c.double().numpy(), w.double().numpy(), 1e-70)
+    want = ol.fp8_round(y)[0] if kind == "fp8" else to_bf16(y).double().numpy()
+    near(got.cpu().double().numpy(), want, y, "rows")

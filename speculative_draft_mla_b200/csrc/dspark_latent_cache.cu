@@ -64,9 +64,13 @@ __device__ __forceinline__ float to_f_sticky(double x) {
     return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// The same of p + e, |e| at most half a unit of p.
+// |x| within 2^-90 .. 2^120
+__device__ __forceinline__ bool middle(float x) {
+    return (__float_as_uint(x) & 0x7fffffffu) - (37u << 23) <= (247u - 37u) << 23;
+}
+// The same of p + e, |e| at most half a unit of p (p not 0, in the middle of fp32's range).
 __device__ __forceinline__ float to_f_sticky(float p, float e) {
-    if (e == 0.f || !(fabsf(p) <= 3.4028235e38f)) return p;
+    if (e == 0.f) return p;
     const uint32_t b = __float_as_uint(p);
     // towards zero where the remainder has the other sign
     return __uint_as_float((((b ^ __float_as_uint(e)) >> 31) ? b - 1 : b) | 1u);
@@ -91,7 +95,7 @@ __device__ __forceinline__ uint32_t e4m3_code(float x) {
 template <typename T, int KIND>
 __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache p, const T *__restrict__ c,
                                                              const T *__restrict__ kr, const T *__restrict__ w,
-                                                             double eps, RopeFreq freq,
+                                                             double eps, double inv_dl, RopeFreq freq,
                                                              const int32_t *__restrict__ pos,
                                                              const int64_t *__restrict__ slots,
                                                              uint8_t *__restrict__ cache, size_t row_bytes) {
@@ -99,31 +103,47 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache
     const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= p.T) return;
     const int64_t slot = slots[t];
-    if (slot < 0 || slot >= (int64_t)p.n_pages * p.page_size) return;  // the whole warp
-    uint8_t *row = cache + (size_t)slot * row_bytes;
+    const int ps = pos[t];
     // lane l holds values 8 l .. 8 l + 7 and, above 256 wide, 256 + 8 l ..
-    constexpr bool kPairs = sizeof(T) == 2;  // squares and x * w are exact in fp32
     float x[2][8];
-    double ss = 0.0;
-    float s1 = 0.f, s2 = 0.f;  // sum of squares and its rounding errors
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const int d = 256 * i + 8 * lane;
         if (d < p.d_l) {
             load8(c + (size_t)t * p.d_l + d, x[i]);
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                if constexpr (kPairs) {
-                    const float q = x[i][k] * x[i][k], n = s1 + q, v = n - s1;
-                    s2 += (s1 - (n - v)) + (q - v);
-                    s1 = n;
-                } else {
-                    ss += (double)x[i][k] * (double)x[i][k];
-                }
-            }
         } else {
 #pragma unroll
             for (int k = 0; k < 8; k++) x[i][k] = 0.f;
+        }
+    }
+    if (slot < 0 || slot >= (int64_t)p.n_pages * p.page_size) return;  // the whole warp
+    uint8_t *row = cache + (size_t)slot * row_bytes;
+    // the rope key: lane l turns pairs l, l + 32 (first: its angles need no other
+    // load, and take their time while the latent's arrive)
+    for (int i = lane; i < p.d_r / 2; i += 32) {
+        const float2 cs = rope_cs(ps, freq.f[i]);
+        const float x0 = to_f(kr[(size_t)t * p.d_r + 2 * i]), x1 = to_f(kr[(size_t)t * p.d_r + 2 * i + 1]);
+        const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
+        if constexpr (KIND == DSPARK_CACHE_F32)
+            *reinterpret_cast<float2 *>(row + 4 * ((size_t)p.d_l + 2 * i)) = make_float2(y0, y1);
+        else
+            *reinterpret_cast<uint32_t *>(row + (KIND == DSPARK_CACHE_FP8 ? (size_t)p.d_l + 4 * i
+                                                                          : 2 * ((size_t)p.d_l + 2 * i))) = bf2(y0, y1);
+    }
+    constexpr bool kPairs = sizeof(T) == 2;  // squares and x * w are exact in fp32
+    double ss = 0.0;
+    float s1 = 0.f, s2 = 0.f;  // sum of squares and its rounding errors
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            if constexpr (kPairs) {
+                const float q = x[i][k] * x[i][k], n = s1 + q, v = n - s1;
+                s2 += (s1 - (n - v)) + (q - v);
+                s1 = n;
+            } else {
+                ss += (double)x[i][k] * (double)x[i][k];
+            }
         }
     }
     double rn = 1.0;
@@ -137,7 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        rn = 1.0 / sqrt(ss / p.d_l + eps);
+        rn = rsqrt(fma(ss, inv_dl, eps));
     }
     const float rh = (float)rn, rl = fabsf(rh) <= 3.4028235e38f ? (float)(rn - (double)rh) : 0.f;
 #pragma unroll
@@ -147,17 +167,43 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache
         if (w && d < p.d_l) {
             float wv[8];
             load8(w + d, wv);
+            // Pairs where u and q lie within 2^-90 .. 2^120 (there they are exact); zeros
+            // and what lies outside in fp64.
+            bool far = !kPairs;
+            if constexpr (kPairs && KIND == DSPARK_CACHE_BF16) {
+                // The product in fp32 is off by 2 units at most: only next to the middle of two
+                // bf16 values (its low half 0x8000, 1 in 8000) does that matter.
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const float u = x[i][k] * wv[k], q = u * rh;
-                // (far from both ends of fp32's range, where the pair is exact)
-                if (kPairs && fabsf(q) <= 1e37f && (fabsf(q) >= 1e-28f || q == 0.f) && fabsf(u) >= 1e-28f &&
-                    fabsf(u) <= 1e37f) {
+                for (int k = 0; k < 8; k++) {
+                    const float u = x[i][k] * wv[k];
+                    z[k] = u * rh;
+                    far |= !middle(u) || !middle(z[k]) || ((__float_as_uint(z[k]) + 4u) & 0xffffu) - 0x8000u <= 8u;
+                }
+            } else if constexpr (kPairs) {
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float u = x[i][k] * wv[k], q = u * rh;
+                    far |= !middle(u) || !middle(q);
                     const float e = fmaf(u, rl, fmaf(u, rh, -q)), sum = q + e, rest = (q - sum) + e;
                     z[k] = KIND == DSPARK_CACHE_F32 ? sum : to_f_sticky(sum, rest);
-                } else {
-                    const double y = (double)x[i][k] * rn * (double)wv[k];
-                    z[k] = KIND == DSPARK_CACHE_F32 ? (float)y : to_f_sticky(y);
+                }
+            }
+            if (far) {
+#pragma unroll 1
+                for (int k = 0; k < 8; k++) {
+                    // (indexed by comparison: the arrays stay in registers)
+                    float xv = 0.f, wk = 0.f;
+#pragma unroll
+                    for (int m = 0; m < 8; m++)
+                        if (m == k) {
+                            xv = x[i][m];
+                            wk = wv[m];
+                        }
+                    const double y = (double)xv * rn * (double)wk;
+                    const float f = KIND == DSPARK_CACHE_F32 ? (float)y : to_f_sticky(y);
+#pragma unroll
+                    for (int m = 0; m < 8; m++)
+                        if (m == k) z[m] = f;
                 }
             }
         } else {
@@ -192,18 +238,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_write(dspark_latent_cache
             else
                 store8(reinterpret_cast<float *>(row) + d, z);
         }
-    }
-    // the rope key: lane l turns pairs l, l + 32
-    const int ps = pos[t];
-    for (int i = lane; i < p.d_r / 2; i += 32) {
-        const float2 cs = rope_cs(ps, freq.f[i]);
-        const float x0 = to_f(kr[(size_t)t * p.d_r + 2 * i]), x1 = to_f(kr[(size_t)t * p.d_r + 2 * i + 1]);
-        const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
-        if constexpr (KIND == DSPARK_CACHE_F32)
-            *reinterpret_cast<float2 *>(row + 4 * ((size_t)p.d_l + 2 * i)) = make_float2(y0, y1);
-        else
-            *reinterpret_cast<uint32_t *>(row + (KIND == DSPARK_CACHE_FP8 ? (size_t)p.d_l + 4 * i
-                                                                          : 2 * ((size_t)p.d_l + 2 * i))) = bf2(y0, y1);
     }
     if constexpr (KIND == DSPARK_CACHE_FP8) {
         const size_t used = (size_t)p.d_l + 2 * p.d_r + 4 * (p.d_l >> 7);
@@ -312,7 +346,7 @@ cudaError_t launch_cache_write(const dspark_latent_cache &p, const void *c, cons
     const size_t rb = cache_row_bytes(p.kind, p.d_l, p.d_r);
     count_launch();
 #define DSPARK_WRITE(T, K)                                                                                       \
-    k_cache_write<T, K><<<grid, kWarps * 32, 0, st>>>(p, (const T *)c, (const T *)kr, (const T *)w, eps, freq, pos, \
+    k_cache_write<T, K><<<grid, kWarps * 32, 0, st>>>(p, (const T *)c, (const T *)kr, (const T *)w, eps, 1.0 / p.d_l, freq, pos, \
                                                       slots, (uint8_t *)cache, rb)
     if (p.dtype == DSPARK_F32) {
         if (p.kind == DSPARK_CACHE_F32) DSPARK_WRITE(float, DSPARK_CACHE_F32);

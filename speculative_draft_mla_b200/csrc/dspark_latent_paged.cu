@@ -15,7 +15,7 @@ namespace {
 // its steps of 64 keys, at least one. The CTA pairs of the
 // attention share all steps evenly, wherever tiles begin and end; first[i] is
 // the tile that pair i begins in. The other CTAs fill the tokens' (cos, sin).
-__global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedPlan w, int tc, int tab_ctas) {
+__global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedPlan w, int tc, int shorts, int tab_ctas) {
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x > 0) {
@@ -39,10 +39,11 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         return;
     }
     __shared__ long long wsteps[32], carry_steps;
-    __shared__ int wtiles[32], carry_tiles, bad, n_split;
+    __shared__ int wtiles[32], carry_tiles, bad, n_split, n_short;
     if (threadIdx.x == 0) {
         bad = 0;
         n_split = 0;
+        n_short = 0;
         carry_steps = 0;
         carry_tiles = 0;
     }
@@ -56,7 +57,15 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         if (s < p.n_seq) {
             v = seq_view(p, s);
             if (v.bad) bad = 1;
-            if (tc) {
+            bool brief = false;
+            if (shorts && v.q_len > 0) {
+                int lo, hi;
+                tile_range(p, v, 0, v.q_len, &lo, &hi);
+                brief = hi - lo <= kShortKeys;
+            }
+            if (brief) {
+                w.short_seq[atomicAdd(&n_short, 1)] = s;
+            } else if (tc) {
                 nt = (v.q_len + w.tpt - 1) / w.tpt;
                 for (int t = 0; t < nt; t++) ns += tile_steps(p, v, t * w.tpt, min(v.q_len, (t + 1) * w.tpt));
                 nt *= w.hchunks;
@@ -123,6 +132,7 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         if (threadIdx.x == 0) {
             w.head->total = total;
             w.head->per = X;
+            w.head->n_short = n_short;
         }
         __syncthreads();
         if (total)
@@ -160,6 +170,7 @@ size_t paged_layout(const Paged &p, void *ws, PagedPlan *w) {
     r.first = (int *)take(sizeof(int) * kPairs);
     r.split = (int *)take(sizeof(int) * kPairs);
     r.tiles = (PagedTile *)take(sizeof(PagedTile) * (size_t)r.max_tiles);
+    r.short_seq = (int *)take(sizeof(int) * (size_t)p.n_seq);
     r.tab = (float2 *)take(sizeof(float2) * 32 * (size_t)p.T);
     r.part_lse = (float *)take(sizeof(float) * 2 * kPairs * 128);
     r.part_o = (float *)take(sizeof(float) * 2 * kPairs * 128 * 512);
@@ -176,10 +187,18 @@ cudaError_t launch_paged(const Paged &pp, void *ws, cudaStream_t st) {
     paged_layout(p, ws, &w);
     const bool run = p.T > 0 && p.n_seq > 0, tc = run && paged_tc_supported(p) && p.n_pages > 0;
     const int tab_ctas = tc ? std::min((p.T + 31) / 32, 296) : 0;
+    // Windows of up to 144 keys: sequences whose tokens see no more than that
+    // together go to the short kernel (drafts of 5 tokens, 128 sequences, window 128:
+    // 170 us without it). Where T tokens of one sequence would fit, all do.
+    const bool shorts = tc && p.window > 0 && p.window <= kShortKeys && (long long)p.n_seq * w.hchunks < (1 << 23);
+    const bool all_short = shorts && (long long)p.window - 1 + p.T <= kShortKeys;
     count_launch();
-    cudaError_t e = launch_pdl(k_paged_plan, dim3(1 + tab_ctas), dim3(1024), 0, st, p, w, tc ? 1 : 0, tab_ctas);
+    cudaError_t e = launch_pdl(k_paged_plan, dim3(1 + tab_ctas), dim3(1024), 0, st, p, w, tc ? 1 : 0, shorts ? 1 : 0,
+                               tab_ctas);
     if (e != cudaSuccess || !run) return e;
-    return tc ? launch_paged_tc(p, w, st) : launch_paged_simt(p, st);
+    if (!tc) return launch_paged_simt(p, st);
+    if (shorts && (e = launch_short_tc(p, w, st)) != cudaSuccess) return e;
+    return all_short ? cudaSuccess : launch_paged_tc(p, w, st);
 }
 
 }  // namespace dspark

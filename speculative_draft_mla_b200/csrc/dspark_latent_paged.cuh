@@ -8,10 +8,12 @@ namespace dspark {
 
 constexpr int kPairs = 74;      // CTA pairs of the tensor-core kernel (two CTAs share a tile's value columns)
 constexpr int kStepKeys = 64;   // keys of a step
+constexpr int kShortKeys = 144; // keys that a sequence of the short kernel sees at most
 
 struct PagedHead {
     long long total, per;  // steps of all tiles; steps of a pair
     int n_split;           // tiles that several pairs work on
+    int n_short;           // sequences of the short kernel
 };
 struct alignas(16) PagedTile {      // up to 128 (token, head) rows of a sequence
     int seq, i0, hc, q_len;  // first token within the sequence, chunk of 128 heads
@@ -23,6 +25,7 @@ struct PagedPlan {
     int *first;            // [kPairs] tile in which pair i begins
     int *split;            // [kPairs] tiles that several pairs work on
     PagedTile *tiles;
+    int *short_seq;        // [n_seq] sequences of the short kernel
     float2 *tab;           // [T, 32] (cos, sin) of the tokens' positions
     float *part_lse, *part_o;  // [2 kPairs, 128], [2 kPairs, 128, 512]: results of parts of a tile
     int tpt, hchunks, max_tiles;  // tokens of a tile, its chunks of heads
@@ -31,6 +34,8 @@ struct PagedPlan {
 bool paged_tc_supported(const Paged &p);
 size_t paged_layout(const Paged &p, void *ws, PagedPlan *w);
 cudaError_t launch_paged_simt(const Paged &p, cudaStream_t st);
+// sequences whose tokens together see few keys (drafts, short windows)
+cudaError_t launch_short_tc(const Paged &p, const PagedPlan &w, cudaStream_t st);
 cudaError_t launch_paged_tc(const Paged &p, const PagedPlan &w, cudaStream_t st);
 
 #ifdef __CUDACC__

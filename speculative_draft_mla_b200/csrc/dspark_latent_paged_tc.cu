@@ -249,6 +249,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (w.head->total == 0) {  // all sequences went to the short kernel
+        if (warp == kWarpM) tmem_dealloc(tmem, 512);
+        return;
+    }
     SegCursor cur;
     cur.begin(w);
     Seg sg;
@@ -827,12 +831,8 @@ cudaError_t launch_paged_tc(const Paged &p, const PagedPlan &w, cudaStream_t st)
     if (p.kind == DSPARK_CACHE_BF16 &&
         (!make_map_nd(&m4, p.cache, 3, dims, strides, b4) || !make_map_nd(&m1, p.cache, 3, dims, strides, b1)))
         return cudaErrorInvalidValue;
-    // queries: 64 columns, heads, tokens (the stride of an extent of one is not used)
     CUtensorMap mq{};
-    const uint64_t qd[3] = {kDL + kDR, (uint64_t)p.n_h, (uint64_t)p.T};
-    const uint64_t qs[2] = {p.n_h > 1 ? 2 * (uint64_t)p.q_hs : 2 * (kDL + kDR), p.T > 1 ? 2 * (uint64_t)p.q_ts : 2 * (kDL + kDR)};
-    const uint32_t qb[3] = {64, (uint32_t)std::min(p.n_h, 128), (uint32_t)w.tpt};
-    if (!make_map_nd(&mq, p.q, 3, qd, qs, qb)) return cudaErrorInvalidValue;
+    if (!make_q_map(&mq, p, w)) return cudaErrorInvalidValue;
     cudaError_t e = p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(m4, m1, mq, p, w, st)
                                                 : launch_t<DSPARK_CACHE_FP8>(m4, m1, mq, p, w, st);
     if (e != cudaSuccess) return e;

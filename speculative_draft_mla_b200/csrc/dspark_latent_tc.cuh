@@ -1,7 +1,7 @@
 // Helpers of the latent-space tensor-core kernels beside dspark_tc_common.cuh.
 #pragma once
 
-#include "dspark_latent.cuh"
+#include "dspark_latent_paged.cuh"
 #include "dspark_tc_common.cuh"
 
 namespace dspark {
@@ -15,6 +15,17 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
                  : "memory");
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
@@ -79,6 +90,15 @@ inline bool make_map_nd(CUtensorMap *m, const void *base, int nd, const uint64_t
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, nd, const_cast<void *>(base), d, s, b, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Queries of the paged attention, a tile's rows of 64 columns: columns, heads,
+// tokens (the stride of an extent of one is not used).
+inline bool make_q_map(CUtensorMap *m, const Paged &p, const PagedPlan &w) {
+    const uint64_t dk = (uint64_t)(p.d_l + p.d_r), d[3] = {dk, (uint64_t)p.n_h, (uint64_t)p.T};
+    const uint64_t s[2] = {p.n_h > 1 ? 2 * (uint64_t)p.q_hs : 2 * dk, p.T > 1 ? 2 * (uint64_t)p.q_ts : 2 * dk};
+    const uint32_t b[3] = {64, (uint32_t)(p.n_h < 128 ? p.n_h : 128), (uint32_t)w.tpt};
+    return make_map_nd(m, p.q, 3, d, s, b);
 }
 
 }  // namespace tc

@@ -227,6 +227,12 @@ PAGED = {
     "draft_block": ([5, 5, 5], [700, 5, 133], 64, 64, 512, 64, False, 128, ("bf16", "fp8")),
     "draft_block_whole": ([5, 5], [200, 777], 128, 64, 512, 64, False, 0, ("bf16", "fp8")),
     "draft_window_one": ([5, 2], [70, 2], 16, 8, 512, 64, False, 1, ("bf16", "fp8")),
+    # windows of which some sequences see more keys together than others: both kernels of one call
+    "mixed_window_draft": ([5, 40, 1, 25, 20], [400, 300, 7, 160, 20], 16, 64, 512, 64, False, 120, ("bf16", "fp8")),
+    "mixed_window_causal": ([3, 60, 1, 30], [400, 300, 7, 160], 16, 20, 512, 64, True, 110, ("bf16", "fp8")),
+    "short_window_many_heads": ([2, 1], [100, 70], 16, 160, 512, 64, True, 33, ("bf16", "fp8")),
+    "short_window_odd_pages": ([7, 3, 2], [77, 123, 300], 5, 20, 512, 64, True, 140, ("bf16", "fp8")),
+    "short_many_sequences": ([2] * 170, [30 + i for i in range(170)], 16, 16, 512, 64, False, 40, ("bf16", "fp8")),
     "odd_pages": ([2, 5], [77, 123], 5, 20, 512, 64, True, 0, ("bf16", "fp8")),
     "page_of_one": ([2], [70], 1, 3, 512, 64, True, 0, ("bf16", "fp8")),
     "many_heads": ([2, 3], [100, 70], 16, 160, 512, 64, True, 0, ("bf16", "fp8")),

@@ -21,8 +21,11 @@
 // twice per tile: for S and dP, and, from L2, for the gradients. (Gradients of a
 // tile interleaved with S and dP of the next share the keys' slices, but need
 // two slots of Q and dO a slice, and with the three that fit the copies' latency
-// is exposed: 4500 cycles a slice against 2700.) What bounds it is the tensor
-// work, 20000 cycles a tile with its short products, and the reductions.
+// is exposed: 4500 cycles a slice against 2700.) What bounds it: shared
+// memory while gradients are formed (of 2900 cycles a slice, the operands of its
+// products take 1440 at 128 bytes a cycle, the copies in 360, dq and dk on their way
+// out 740), and the copies' latency while S and dP are (1900 a slice, 16000 a
+// tile of 44000).
 //
 // Sums of key gradients are fp32 in whatever order the tiles finish: two runs
 // may differ in the last bits before the rounding to bf16. P and dS are bf16
@@ -80,6 +83,12 @@ struct Args {
 __device__ __forceinline__ void red4(float *a, float x, float y, float z, float w) {
     asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
+// A box of shared memory added to fp32 rows.
+__device__ __forceinline__ void tma_red_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)m),
+                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 __device__ __forceinline__ void red1(float *a, float x) {
     asm volatile("red.global.add.f32 [%0], %1;" ::"l"(a), "f"(x) : "memory");
 }
@@ -121,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_c,
                  const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_l,
                  const __grid_constant__ CUtensorMap tm_c5, const __grid_constant__ CUtensorMap tm_h5,
-                 const __grid_constant__ CUtensorMap tm_l5, const __grid_constant__ CUtensorMap tm_dq, const Args p) {
+                 const __grid_constant__ CUtensorMap tm_l5, const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_acc, const Args p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     // a slot's full barriers: [0] of copies for the gradients, [1] of those for the scores
@@ -538,9 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < kBlock; e++) red1(dd + (size_t)e * kDK + 64 * c, d[e]);
                 }
             } else {
-                // dk: the warp's 32 key slots, 32 columns at a time through shared memory, so
-                // that a reduction adds whole 128-byte lines of four rows (rows one to a
-                // lane, 16 or 32 bytes of a line each, took 2.5 times as long)
+                // dk: the warp's 32 key slots, 32 columns at a time through shared memory, a
+                // box that one copy adds to the accumulators. (Added by the lanes from there,
+                // whole lines each, 3% slower; rows one to a lane, 16 or 32 bytes of a line
+                // each, 15%, although that spares shared memory the trip.) Rows past the
+                // block's own keys add zero.
                 const int first = cur.a - (p.W - 1);
                 float *base = p.dacc + (size_t)cur.b * p.L * kDK;
                 uint8_t *stg = sm + oT + q4 * 4096;
@@ -557,26 +568,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&kcfree[buf]);
+                    if (32 * q4 >= p.W - 1 || first + 32 * q4 + 31 < 0) continue;
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        __syncwarp();
-#pragma unroll
-                        for (int u = 0; u < 8; u++)
-                            *reinterpret_cast<float4 *>(stg + sw128(lane, u)) =
-                                make_float4(v[h][4 * u], v[h][4 * u + 1], v[h][4 * u + 2], v[h][4 * u + 3]);
+                        if (lane == 0) bulk_wait_read_all();
                         __syncwarp();
 #pragma unroll
                         for (int u = 0; u < 8; u++) {
-                            const int row = 4 * u + (lane >> 3), slot = 32 * q4 + row, pos = first + slot;
-                            const float4 x = *reinterpret_cast<const float4 *>(stg + sw128(row, lane & 7));
-                            if (slot < p.W - 1 && pos >= 0)
-                                red4(base + (size_t)pos * kDK + 64 * c + 32 * h + 4 * (lane & 7), x.x, x.y, x.z, x.w);
+                            const float *x = &v[h][4 * u];
+                            *reinterpret_cast<float4 *>(stg + sw128(lane, u)) =
+                                32 * q4 + lane < p.W - 1 ? make_float4(x[0], x[1], x[2], x[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        if (first + 32 * q4 >= 0) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_red_3d(&tm_acc, stg, 64 * c + 32 * h, first + 32 * q4, cur.b);
+                                bulk_commit();
+                            }
+                        } else {  // (a box may not start before the first row)
+                            __syncwarp();
+#pragma unroll 1
+                            for (int u = 0; u < 8; u++) {
+                                const int row = 4 * u + (lane >> 3), slot = 32 * q4 + row, pos = first + slot;
+                                const float4 x = *reinterpret_cast<const float4 *>(stg + sw128(row, lane & 7));
+                                if (slot < p.W - 1 && pos >= 0)
+                                    red4(base + (size_t)pos * kDK + 64 * c + 32 * h + 4 * (lane & 7), x.x, x.y, x.z, x.w);
+                            }
                         }
                     }
                 }
             }
         }
     }
+
+    if (warp >= 4 && warp < 8 && lane == 0) bulk_wait_all();
 
     // ---------------------------------------------------------- teardown
     __syncthreads();
@@ -600,6 +626,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc(tmem, 512);
     }
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
+}
+
+// The accumulators as boxes of 32 rows x 32 columns.
+bool make_acc_map(CUtensorMap *m, float *acc, uint64_t L, uint64_t B) {
+    auto fn = encode_fn();
+    const cuuint64_t d[3] = {kDK, L, B}, s[2] = {kDK * 4, L * kDK * 4};
+    const cuuint32_t b[3] = {32, 32, 1}, es[3] = {1, 1, 1};
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, acc, d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The queries' rope slices turned to their positions, hi then lo, and the
@@ -703,7 +739,7 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
         a.dacc = ws.dacc;
         a.err = ws.base.err;
         a.wait_ns = p.wait_ns;
-        CUtensorMap mq, mg, mr, mc, mh, ml, mc5, mh5, ml5, mdq;
+        CUtensorMap mq, mg, mr, mc, mh, ml, mc5, mh5, ml5, mdq, macc;
         const uint64_t L = p.L, B = p.B, R = p.R, H = p.n_h;
         const uint64_t qd[4] = {kDK, R, H, B}, qs[3] = {kDK * 2, R * kDK * 2, H * R * kDK * 2};
         const uint64_t gd[4] = {kDL, R, H, B}, gs[3] = {kDL * 2, R * kDL * 2, H * R * kDL * 2};
@@ -716,13 +752,13 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
             !make_map_nd(&mr, ws.q_rot, 4, sd, ss, qb) || !make_map_nd(&mc, c, 3, cd, cs, wb) ||
             !make_map_nd(&mh, ws.kr_hi, 3, rd, rs, wb) || !make_map_nd(&mc5, c, 3, cd, cs, db) ||
             !make_map_nd(&mh5, ws.kr_hi, 3, rd, rs, db) || !make_map_nd(&ml, ws.kr_lo, 3, rd, rs, wb) ||
-            !make_map_nd(&ml5, ws.kr_lo, 3, rd, rs, db))
+            !make_map_nd(&ml5, ws.kr_lo, 3, rd, rs, db) || !make_acc_map(&macc, ws.dacc, L, B))
             return cudaErrorInvalidValue;
         e = cudaFuncSetAttribute(k_lat_bwd_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         count_launch();
         e = launch_pdl(k_lat_bwd_tc, dim3(std::min(a.n_work, nsm)), dim3(kThreads), kSmem, st, mq, mg, mr, mc, mh, ml,
-                       mc5, mh5, ml5, mdq, a);
+                       mc5, mh5, ml5, mdq, macc, a);
         if (e != cudaSuccess) return e;
     }
     count_launch();

@@ -71,7 +71,8 @@ DSPARK_API dspark_status dspark_latent_attn_fwd(const dspark_latent_problem *p, 
 /* Backward for a loss L with dL/dO = do_: writes dq, dc (the latent's gradient
  * as key and as value) and dkr, with respect to the un-rotated inputs. lse is
  * the forward's. The forward's O is not needed: rowsum(dO o O) is formed as
- * sum_k P_k dP_k. */
+ * sum_k P_k dP_k. dc and dkr are fp32 sums over heads and blocks, in an order that
+ * may differ between runs, rounded once. */
 DSPARK_API dspark_status dspark_latent_attn_bwd(const dspark_latent_problem *p, const void *q, const void *c,
                                                 const void *kr, const int32_t *anchors, const uint8_t *keep,
                                                 const float *lse, const void *do_, void *dq, void *dc, void *dkr,
@@ -147,8 +148,8 @@ DSPARK_API dspark_status dspark_latent_cache_read(const dspark_latent_cache *p, 
  * Limits: n_h >= 1, n_seq >= 0, T >= 0, page_size >= 1, widths as the cache,
  *   T * n_h < 2^31, max_pages * page_size < 2^31, n_pages * page_size < 2^31,
  *   n_seq < 2^24, window >= 0.
- * max_kv_len, a bound of kv_len known to the caller, only sets how the keys are
- * split over the GPU (0 = max_pages * page_size). */
+ * max_kv_len, a bound of kv_len known to the caller (0 = max_pages * page_size),
+ * only guides the choice of kernels: a wrong one costs time, not results. */
 typedef struct {
     int32_t n_seq, T, n_h, d_l, d_r;
     int32_t page_size, n_pages, max_pages;

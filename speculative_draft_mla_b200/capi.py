@@ -517,6 +517,8 @@ def _paged(q, cache, block_table, max_kv_len, d_l, d_r, scale, causal, window, r
         a, b, c = t.stride()
         if c != 1:
             raise ValueError("%s must be contiguous in its last dimension" % name)
+        if (a == 0 and T > 1) or (b == 0 and n_h > 1):  # (two zeros stand for contiguous)
+            raise ValueError("%s must not repeat tokens or heads" % name)
         return a, b
 
     n_seq, max_pages = block_table.shape

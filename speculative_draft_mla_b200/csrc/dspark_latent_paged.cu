@@ -187,11 +187,16 @@ cudaError_t launch_paged(const Paged &pp, void *ws, cudaStream_t st) {
     paged_layout(p, ws, &w);
     const bool run = p.T > 0 && p.n_seq > 0, tc = run && paged_tc_supported(p) && p.n_pages > 0;
     const int tab_ctas = tc ? std::min((p.T + 31) / 32, 296) : 0;
-    // Windows of up to 144 keys: sequences whose tokens see no more than that
-    // together go to the short kernel (drafts of 5 tokens, 128 sequences, window 128:
-    // 170 us without it). Where T tokens of one sequence would fit, all do.
-    const bool shorts = tc && p.window > 0 && p.window <= kShortKeys && (long long)p.n_seq * w.hchunks < (1 << 23);
-    const bool all_short = shorts && (long long)p.window - 1 + p.T <= kShortKeys;
+    // Sequences whose tokens see up to 144 keys together go to the short kernel
+    // (drafts of 5 tokens, 128 sequences, window 128: 50 us, 170 without it; 128
+    // tokens over up to 144 keys each, no window: 21 and 47 us; one token: 17 and
+    // 18.5). It is launched where the window or the bound of kv_len makes such
+    // sequences likely, and alone where no sequence can see more.
+    const auto at_most = [](long long n) { return n <= kShortKeys; };
+    const bool shorts = tc && ((p.window > 0 && at_most(p.window)) || at_most(p.max_kv)) &&
+                        (long long)p.n_seq * w.hchunks < (1 << 23);
+    const bool all_short = shorts && ((p.window > 0 && at_most((long long)p.window - 1 + p.T)) ||
+                                      at_most((long long)p.max_pages * p.page_size));
     count_launch();
     cudaError_t e = launch_pdl(k_paged_plan, dim3(1 + tab_ctas), dim3(1024), 0, st, p, w, tc ? 1 : 0, shorts ? 1 : 0,
                                tab_ctas);

@@ -164,7 +164,10 @@ __device__ __forceinline__ bool load_q(const Paged &p, const PagedPlan &w, const
     }
     tmem_st32u(trow + kColR, x);
     tmem_st32u(trow + kColR + 32, lo);
-    if (!warp_all(mbar_wait(land, 0, abort_flag, wlim))) return false;  // (its even phase)
+    if (!warp_all(mbar_wait(land, 0, abort_flag, wlim))) {  // (its even phase)
+        tmem_wait_st();  // tensor memory is about to be released
+        return false;
+    }
 #pragma unroll
     for (int c = 0; c < 4; c++) {
 #pragma unroll

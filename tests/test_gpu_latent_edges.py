@@ -1,0 +1,169 @@
+"""The latent operators at their edges: waits that run out, calls at the same time on two streams, pages shared by
+sequences, bounds of kv_len that choose other kernels, refused tensors."""
+import pytest
+import torch
+
+import latent_parity as lp
+from speculative_draft_mla_b200 import build as dbuild
+from speculative_draft_mla_b200 import capi
+from test_gpu_latent_attn import make, run
+from test_gpu_latent_cache import filled, plan, reference
+
+pytestmark = pytest.mark.gpu
+ERR_DEVICE = 7
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    dbuild.build()
+    return capi.load()
+
+
+def _runs_out(call):
+    """call (returning its workspace) with waits of 1 ns: the device error, and only once."""
+    prev = capi.set_wait_limit_ns(1)
+    try:
+        ws = call()
+        with pytest.raises(capi.DsparkError) as e:
+            capi.get_error(ws)
+        assert e.value.status == ERR_DEVICE
+    finally:
+        assert capi.set_wait_limit_ns(prev) == 1
+    capi.get_error(ws)
+
+
+def _close(a, b):
+    # fp32 sums of tiles' contributions in any order, rounded to bf16
+    a, b = a.float(), b.float()
+    assert ((a - b).abs() <= torch.maximum(a.abs(), b.abs()) * 2.0 ** -7 + 1e-5).all()
+
+
+def test_draft_waits_run_out_and_the_context_recovers():
+    S, W = 300, 128
+    t = make(5, 1, S, 40, 64, 512, 64, "bf16")
+    before = run(t, S, W)
+    d = {k: v.cuda() for k, v in t.items()}
+    _runs_out(lambda: capi.latent_attn_fwd(d["q"], d["c"], d["kr"], d["an"], d["kp"], S, W)[2])
+
+    def bwd():
+        ws = capi.alloc_latent_workspace(capi.latent_problem(1, 64, S, 40, W), "cuda")
+        capi.latent_attn_bwd(d["q"], d["c"], d["kr"], d["an"], d["kp"], before["lse"], d["dout"], S, W, workspace=ws)
+        return ws
+
+    _runs_out(bwd)
+    after = run(t, S, W)
+    for k in ("o", "lse", "dq"):
+        assert torch.equal(before[k], after[k]), k
+    for k in ("dc", "dkr"):
+        _close(before[k], after[k])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("name", ["long", "short"])
+def test_paged_waits_run_out_and_the_context_recovers(name, kind):
+    q_lens, kv_lens, window = ([1, 4], [3000, 2500], 0) if name == "long" else ([5] * 64, [200] * 64, 128)
+    n_pages, table, qs, kv = plan(71, q_lens, kv_lens, 16)
+    cache, _, _ = filled(72, kind, n_pages, 16, 512, 64)
+    q = torch.randn(sum(q_lens), 64, 576, generator=torch.Generator().manual_seed(73)).to(torch.bfloat16).cuda()
+    args = (q, cache, table.cuda(), qs.cuda(), kv.cuda())
+    o, lse, ws = capi.latent_attn_paged(*args, window=window)
+    capi.get_error(ws)
+    _runs_out(lambda: capi.latent_attn_paged(*args, window=window)[2])
+    o2, lse2, ws = capi.latent_attn_paged(*args, window=window)
+    capi.get_error(ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_bounds_of_kv_len_choose_kernels_not_results(kind, causal):
+    """Sequences of up to 144 keys without a window: by the table's width, by a bound, by a wrong bound."""
+    q_lens, kv_lens, page, n_h = [1, 5, 0, 7, 144, 2], [144, 9, 33, 7, 144, 0], 16, 24
+    n_pages, table, qs, kv = plan(81, q_lens, kv_lens, page)
+    cache, lat, rope = filled(82, kind, n_pages, page, 512, 64)
+    q = torch.randn(sum(q_lens), n_h, 576, generator=torch.Generator().manual_seed(83)).to(torch.bfloat16)
+    val, err = reference(q.double().numpy(), lat, rope, table.numpy(), qs.numpy(), kv.numpy(), page,
+                         capi.LATENT_SCALE, causal, 0, True)
+    wide = torch.full((len(kv_lens), 40), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    for t, bound in ((table, 0), (table, 144), (wide, 0), (wide, 144), (wide, 20), (wide, 145)):
+        o, lse, ws = capi.latent_attn_paged(q.cuda(), cache, t.cuda(), qs.cuda(), kv.cuda(), bound, causal=causal)
+        capi.get_error(ws)
+        lp.check("o", o, val["o"], err["o"])
+        lp.check("lse", lse, val["lse"], err["lse"])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("window", [0, 100])
+def test_sequences_share_pages(kind, window):
+    """A common beginning stored once, a page named twice within a sequence's table too."""
+    page, n_h = 16, 16
+    cache, lat, rope = filled(92, kind, 24, page, 512, 64)
+    table = torch.tensor([[3, 7, 5, 11, 3, 9, 2, 1, 0, 20, 21, 8], [3, 7, 5, 11, 3, 9, 2, 1, 0, 22, 23, 4]],
+                         dtype=torch.int32)
+    qs, kv = torch.tensor([0, 3, 4], dtype=torch.int32), torch.tensor([190, 170], dtype=torch.int32)
+    q = torch.randn(4, n_h, 576, generator=torch.Generator().manual_seed(93))
+    q = q.to(torch.float32 if kind == "f32" else torch.bfloat16)
+    val, err = reference(q.double().numpy(), lat, rope, table.numpy(), qs.numpy(), kv.numpy(), page,
+                         capi.LATENT_SCALE, True, window, kind != "f32")
+    o, lse, ws = capi.latent_attn_paged(q.cuda(), cache, table.cuda(), qs.cuda(), kv.cuda(), window=window)
+    capi.get_error(ws)
+    lp.check("o", o, val["o"], err["o"])
+    lp.check("lse", lse, val["lse"], err["lse"])
+
+
+def test_calls_at_the_same_time_on_two_streams():
+    """Different problems of every operator, each stream with workspaces of its own."""
+    S, W = 260, 100
+    drafts = [make(100 + i, 1, S, 30 + i, 20 + 6 * i, 512, 64, "bf16") for i in range(2)]
+    page = 16
+    n_pages, table, qs, kv = plan(101, [2, 5], [300, 180], page)
+    cache, _, _ = filled(102, "fp8", n_pages, page, 512, 64)
+    q = [torch.randn(7, 64, 576, generator=torch.Generator().manual_seed(103 + i)).to(torch.bfloat16).cuda()
+         for i in range(2)]
+    args = (cache, table.cuda(), qs.cuda(), kv.cuda())
+
+    def work(i):
+        out = run(drafts[i], S, W)
+        out["p"], out["pl"], ws = capi.latent_attn_paged(q[i], *args, window=130 * i)
+        return out, ws
+
+    alone = [work(i)[0] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    dev = [{k: v.cuda() for k, v in t.items()} for t in drafts]
+    torch.cuda.synchronize()
+    for rep in range(3):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                d = dev[i]
+                o, lse, ws = capi.latent_attn_fwd(d["q"], d["c"], d["kr"], d["an"], d["kp"], S, W)
+                dq, dc, dkr = capi.latent_attn_bwd(d["q"], d["c"], d["kr"], d["an"], d["kp"], lse, d["dout"], S, W,
+                                                   workspace=ws, flags=capi.FLAG_REUSE_DESCRIPTOR)
+                p, pl, pws = capi.latent_attn_paged(q[i], *args, window=130 * i)
+                got[i] = dict(o=o, lse=lse, dq=dq, dc=dc, dkr=dkr, p=p, pl=pl, ws=ws, pws=pws)
+        torch.cuda.synchronize()
+        for i in range(2):
+            capi.get_error(got[i].pop("ws"))
+            capi.get_error(got[i].pop("pws"))
+            for k, x in got[i].items():
+                if k in ("dc", "dkr"):
+                    _close(x, alone[i][k])
+                else:
+                    assert torch.equal(x, alone[i][k]), k
+
+
+def test_repeated_tokens_or_heads_are_refused():
+    cache = capi.latent_cache(4, 16)
+    table = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    qs, kv = torch.tensor([0, 2], dtype=torch.int32).cuda(), torch.tensor([20], dtype=torch.int32).cuda()
+    one = torch.zeros(1, 1, 576, dtype=torch.bfloat16, device="cuda")
+    for q in (one.expand(2, 8, 576), one.expand(1, 8, 576), one.expand(2, 1, 576)):
+        with pytest.raises(ValueError):
+            capi.latent_attn_paged(q, cache, table, qs, kv)
+    q = torch.zeros(2, 8, 576, dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros(1, 1, 512, dtype=torch.bfloat16, device="cuda").expand(2, 8, 512)
+    with pytest.raises(ValueError):
+        capi.latent_attn_paged(q, cache, table, qs, kv, out=(o, torch.zeros(2, 8, device="cuda")))

@@ -165,3 +165,16 @@ def test_binding_refusals():
                                z(1, dtype=torch.int32))
     with pytest.raises(capi.DsparkError):
         capi.latent_cache(2, 4, d_l=500, device="cpu")
+
+
+def test_paged_limits_of_sizes_and_strides(lib):
+    for kw in (dict(n_pages=2 ** 27, page_size=16), dict(n_pages=2 ** 30, page_size=2, max_pages=0),
+               dict(n_h=2 ** 29), dict(q_token_stride=1 << 40, q_head_stride=576)):
+        assert capi.latent_paged_workspace_size(paged_p(**kw)) == 0, kw
+    for kw in (dict(q_token_stride=0, q_head_stride=576), dict(q_token_stride=576 * 64, q_head_stride=0),
+               dict(o_token_stride=0, o_head_stride=512), dict(o_token_stride=512 * 64, o_head_stride=0)):
+        p = paged_p(**kw)
+        assert capi.latent_paged_workspace_size(p) == 0, kw
+        assert lib.dspark_latent_attn_paged(ctypes.byref(p), *[FAKE] * 8, 1 << 30, None) == SHAPE, kw
+    # the stride of an extent of one is not used
+    assert capi.latent_paged_workspace_size(paged_p(T=1, q_token_stride=0, q_head_stride=576)) > 0

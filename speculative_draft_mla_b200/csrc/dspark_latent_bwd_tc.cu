@@ -265,114 +265,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------------------------------------------- MMAs
         // Three issuers (one thread of each warp), as a single thread issuing all
         // products was slower than the products: 0 S and dP, 1 dq, 2 dk and dd.
-        if (lane == 0) {
-            const int who = warp - kWarpM;
-            const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0), idQ = idesc_bf16(128, 64, 1);
-            const uint32_t idK = idesc_bf16_ab(128, 64, 1, 1), idD = idesc_bf16_ab(128, 32, 1, 0);
-            const int ksc = p.ctxpad / 16, ksr = (p.hp * kBlock + 15) / 16;
-            const SDesc dsr = sdesc_split(sdesc_sw128(smem_u32(sm + oDS), 16, 1024));         // rows x keys
-            const SDesc dst = sdesc_split(sdesc_sw128(smem_u32(sm + oDS), kSlot, 1024));      // keys x rows
-            const SDesc pt = sdesc_split(sdesc_sw128(smem_u32(sm + oPr), kSlot, 1024));
-            const SDesc dda = sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 32 * 128, 1024));   // rows x draft keys
-            const SDesc ddb = sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 16, 1024));         // draft keys x rows
-            TileCursor cu(p);
-            Tile cur;
-            bool ok = true;
-            uint32_t i = 0, k = 0;  // slices of gradients; tiles
-            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait(bar, parity, abort_flag, wlim); };
-            // Copy n of a ring, of a kind: its slot, once it has landed. A parity tells a
-            // barrier's phase from the one before only, so copies for the scores and for
-            // the gradients, which have other users, have barriers of their own (a user
-            // that skipped a copy on a shared one could pass a phase early).
-            uint32_t kph = 0, qph = 0;
-            auto take_k = [&](int kind, uint32_t n) {
-                const uint32_t s = n % kKSlots;
-                wait(&kfull[kind * kKSlots + s], (kph >> s) & 1);
-                kph ^= 1u << s;
-                return s;
-            };
-            auto take_q = [&](int kind, uint32_t n) {
-                const uint32_t s = n % kPairs2;
-                wait(&qfull[kind * kPairs2 + s], (qph >> s) & 1);
-                qph ^= 1u << s;
-                return s;
-            };
-            for (; ok && cu.next(p, cur); k++) {
-                const uint32_t kn = k * (2 * kSlices + 1), qn = k * 2 * kSlices;  // the tile's first copies
-                if (who == 0) {
-                    // S and dP of the tile before are read
-                    if (k > 0 && !wait(pds, (k - 1) & 1)) break;
+        const int who = (int)uniform((uint32_t)(warp - kWarpM));
+        const uint32_t tm = uniform(tmem);
+        const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0), idQ = idesc_bf16(128, 64, 1);
+        const uint32_t idK = idesc_bf16_ab(128, 64, 1, 1), idD = idesc_bf16_ab(128, 32, 1, 0);
+        const int ksc = p.ctxpad / 16, ksr = (p.hp * kBlock + 15) / 16;
+        const SDesc dsr = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDS), 16, 1024)));         // rows x keys
+        const SDesc dst = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDS), kSlot, 1024)));      // keys x rows
+        const SDesc pt = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oPr), kSlot, 1024)));
+        const SDesc dda = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 32 * 128, 1024)));   // rows x draft keys
+        const SDesc ddb = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 16, 1024)));         // draft keys x rows
+        // slots of keys, and of Q and dO, as rows x columns and transposed
+        const SDesc sk = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oK), 16, 1024)));
+        const SDesc vk = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oK), kKSlot, 1024)));
+        const SDesc sq = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oPair), 16, 1024)));
+        const SDesc vq = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oPair), kSlot, 1024)));
+        TileCursor cu(p);
+        Tile cur;
+        bool ok = true;
+        uint32_t i = 0, k = 0;  // slices of gradients; tiles
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return ok = ok && warp_all(mbar_wait(bar, parity, abort_flag, wlim));
+        };
+        // Copy n of a ring, of a kind: its slot, once it has landed. A parity tells a
+        // barrier's phase from the one before only, so copies for the scores and for
+        // the gradients, which have other users, have barriers of their own (a user
+        // that skipped a copy on a shared one could pass a phase early).
+        uint32_t kph = 0, qph = 0;
+        auto take_k = [&](int kind, uint32_t n) {
+            const uint32_t s = n % kKSlots;
+            wait(&kfull[kind * kKSlots + s], (kph >> s) & 1);
+            kph ^= 1u << s;
+            return s;
+        };
+        auto take_q = [&](int kind, uint32_t n) {
+            const uint32_t s = n % kPairs2;
+            wait(&qfull[kind * kPairs2 + s], (qph >> s) & 1);
+            qph ^= 1u << s;
+            return s;
+        };
+        for (; ok && cu.next(p, cur); k++) {
+            const uint32_t kn = k * (2 * kSlices + 1), qn = k * 2 * kSlices;  // the tile's first copies
+            if (who == 0) {
+                // S and dP of the tile before are read
+                if (k > 0 && !wait(pds, (k - 1) & 1)) break;
 #pragma unroll 1
-                    for (int c = 0; c < kSlices; c++) {
-                        const uint32_t ks = take_k(1, kn + c), qs = take_q(1, qn + c);
+                for (int c = 0; c < kSlices; c++) {
+                    const uint32_t ks = take_k(1, kn + c), qs = take_q(1, qn + c);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const SDesc kd = sdesc_plus(sk, ks * kKSlot);
+                    const SDesc qd = sdesc_plus(sq, qs * kPair);
+                    const SDesc gd = sdesc_plus(sq, qs * kPair + kSlot);
+                    // the second product: dP; of the rope slice, S again with Q's lo
+                    const uint32_t d2 = tm + (c < 8 ? kColP : kColS);
+#pragma unroll
+                    for (int s = 0; s < 4; s++) mma_bf16_ss_warp(tm + kColS, qd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
+#pragma unroll
+                    for (int s = 0; s < 4; s++) mma_bf16_ss_warp(d2, gd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
+                    mma_commit_warp(&kempty[ks]);
+                    if (c == kSlices - 1) {  // Q's hi with the keys' lo
+                        const uint32_t kl = take_k(1, kn + kSlices);
                         if (!ok) break;
                         tc_fence_after();
-                        const SDesc kd = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), 16, 1024));
-                        const SDesc qd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), 16, 1024));
-                        const SDesc gd = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), 16, 1024));
-                        // the second product: dP; of the rope slice, S again with Q's lo
-                        const uint32_t d2 = tmem + (c < 8 ? kColP : kColS);
+                        const SDesc ld = sdesc_plus(sk, kl * kKSlot);
 #pragma unroll
-                        for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
-#pragma unroll
-                        for (int s = 0; s < 4; s++) mma_bf16_ss(d2, gd.at(2 * s), kd.at(2 * s), idS, (c | s) != 0);
-                        mma_commit(&kempty[ks]);
-                        if (c == kSlices - 1) {  // Q's hi with the keys' lo
-                            const uint32_t kl = take_k(1, kn + kSlices);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const SDesc ld = sdesc_split(sdesc_sw128(smem_u32(sm + oK + kl * kKSlot), 16, 1024));
-#pragma unroll
-                            for (int s = 0; s < 4; s++) mma_bf16_ss(tmem + kColS, qd.at(2 * s), ld.at(2 * s), idS, 1u);
-                            mma_commit(&kempty[kl]);
-                        }
-                        mma_commit(&qempty[qs]);
+                        for (int s = 0; s < 4; s++) mma_bf16_ss_warp(tm + kColS, qd.at(2 * s), ld.at(2 * s), idS, 1u);
+                        mma_commit_warp(&kempty[kl]);
                     }
-                    if (ok) mma_commit(sfull);
-                    continue;
+                    mma_commit_warp(&qempty[qs]);
                 }
-                if (!wait(pds, k & 1)) break;  // P and dS are written
+                if (ok) mma_commit_warp(sfull);
+                continue;
+            }
+            if (!wait(pds, k & 1)) break;  // P and dS are written
 #pragma unroll 1
-                for (int c = 0; c < kSlices; c++, i++) {
-                    if (who == 1) {
-                        const uint32_t ks = take_k(0, kn + kSlices + 1 + c);
-                        if (!ok || (i > 0 && !wait(qcfree, (i - 1) & 1))) break;
-                        tc_fence_after();
-                        const uint32_t d = tmem + kColC;
-                        const SDesc kv = sdesc_split(sdesc_sw128(smem_u32(sm + oK + ks * kKSlot), kKSlot, 1024));
-                        // (unrolled: a product of 64 columns takes 50 cycles, a step of a rolled loop 90)
+            for (int c = 0; c < kSlices; c++, i++) {
+                if (who == 1) {
+                    const uint32_t ks = take_k(0, kn + kSlices + 1 + c);
+                    if (!ok || (i > 0 && !wait(qcfree, (i - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t d = tm + kColC;
+                    const SDesc kv = sdesc_plus(vk, ks * kKSlot);
+                    // (unrolled: a product of 64 columns takes 50 cycles, a step of a rolled loop 90)
 #pragma unroll
-                        for (int s = 0; s < 8; s++)
-                            if (s < ksc) mma_bf16_ss(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
-                        mma_bf16_ss(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
-                        mma_commit(&kempty[ks]);
-                        if (c == kSlices - 1) mma_commit(&done[0]);
-                        mma_commit(qcfull);  // last: nothing is in flight once its reader has it
-                    } else {
-                        const uint32_t qs = take_q(0, qn + kSlices + c), buf = i & 1;
-                        if (!ok || (i > 1 && !wait(&kcfree[buf], ((i >> 1) - 1) & 1))) break;
-                        tc_fence_after();
-                        const SDesc qb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair), kSlot, 1024));
-                        const SDesc gb = sdesc_split(sdesc_sw128(smem_u32(sm + oPair + qs * kPair + kSlot), kSlot, 1024));
-                        const uint32_t d = tmem + kColC + 64 + 64 * buf;
-                        const SDesc p2 = c < 8 ? pt : dst;
+                    for (int s = 0; s < 8; s++)
+                        if (s < ksc) mma_bf16_ss_warp(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
+                    mma_bf16_ss_warp(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
+                    mma_commit_warp(&kempty[ks]);
+                    if (c == kSlices - 1) mma_commit_warp(&done[0]);
+                    mma_commit_warp(qcfull);  // last: nothing is in flight once its reader has it
+                } else {
+                    const uint32_t qs = take_q(0, qn + kSlices + c), buf = i & 1;
+                    if (!ok || (i > 1 && !wait(&kcfree[buf], ((i >> 1) - 1) & 1))) break;
+                    tc_fence_after();
+                    const SDesc qb = sdesc_plus(vq, qs * kPair);
+                    const SDesc gb = sdesc_plus(vq, qs * kPair + kSlot);
+                    const uint32_t d = tm + kColC + 64 + 64 * buf;
+                    const SDesc p2 = c < 8 ? pt : dst;
 #pragma unroll
-                        for (int s = 0; s < kRows / 16; s++) {
-                            if (s >= ksr) continue;
-                            mma_bf16_ss(d, dst.at(128 * s), qb.at(128 * s), idK, s > 0);
-                            mma_bf16_ss(d, p2.at(128 * s), gb.at(128 * s), idK, 1u);
-                        }
-                        mma_commit(&kcfull[buf]);
-                        if (i > 0 && !wait(dfree, (i - 1) & 1)) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int s = 0; s < kRows / 16; s++)
-                            if (s < ksr)
-                                mma_bf16_ss(tmem + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
-                        mma_commit(&qempty[qs]);
-                        if (c == kSlices - 1) mma_commit(&done[1]);
-                        mma_commit(dfull);  // last
+                    for (int s = 0; s < kRows / 16; s++) {
+                        if (s >= ksr) continue;
+                        mma_bf16_ss_warp(d, dst.at(128 * s), qb.at(128 * s), idK, s > 0);
+                        mma_bf16_ss_warp(d, p2.at(128 * s), gb.at(128 * s), idK, 1u);
                     }
+                    mma_commit_warp(&kcfull[buf]);
+                    if (i > 0 && !wait(dfree, (i - 1) & 1)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < kRows / 16; s++)
+                        if (s < ksr)
+                            mma_bf16_ss_warp(tm + kColD, qb.at(128 * s), ddb.at((s >> 2) * (32 * 8) + (s & 3) * 2), idD, s > 0);
+                    mma_commit_warp(&qempty[qs]);
+                    if (c == kSlices - 1) mma_commit_warp(&done[1]);
+                    mma_commit_warp(dfull);  // last
                 }
             }
         }
@@ -606,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---------------------------------------------------------- teardown
     __syncthreads();
+    if (*abort_flag && warp >= kWarpM && warp < kWarpO) mma_commit_warp(&drain[warp - kWarpM]);
     if (*abort_flag && lane == 0) {
         volatile int never = 0;
         const uint32_t ring = warp == kWarpK ? kKSlots : kPairs2;
@@ -614,10 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t s = 0; s < ring; s++)
                 for (int kind = 0; kind < 2; kind++)
                     if ((n_used[kind] >> s) & 1) mbar_wait(&full[kind * ring + s], ((n_phase[kind] >> s) & 1) ^ 1, &never);
-        if (warp >= kWarpM && warp < kWarpO) {
-            mma_commit(&drain[warp - kWarpM]);
-            mbar_wait(&drain[warp - kWarpM], 0, &never);
-        }
+        if (warp >= kWarpM && warp < kWarpO) mbar_wait(&drain[warp - kWarpM], 0, &never);
     }
     tc_fence_before();
     __syncthreads();

@@ -435,71 +435,70 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         }
     } else if (warp == kWarpM) {
         // ------------------------------------------------------ S = Q K^T
-        {
-            const uint32_t idS = idesc_bf16(128, kStepKeys, 0), tm = uniform(tmem), dS = tm + kColS;
-            const SDesc qd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oQ), 16, 1024)));
-            uint32_t g = 0, k = 0;
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && warp_all(mbar_wait(bar, parity, abort_flag, wlim)); };
-            // latent slices 0 - 3 (Q in tensor memory) or 4 - 7 (Q in shared memory); kd: the first of the four
-            auto four = [&](const SDesc &kd, bool upper, bool first) {
-                if (upper) {
+        const uint32_t idS = idesc_bf16(128, kStepKeys, 0), tm = uniform(tmem), dS = tm + kColS;
+        const SDesc qd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oQ), 16, 1024)));
+        uint32_t g = 0, k = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return ok = ok && warp_all(mbar_wait(bar, parity, abort_flag, wlim));
+        };
+        // latent slices 0 - 3 (Q in tensor memory) or 4 - 7 (Q in shared memory); kd: the first of the four
+        auto four = [&](const SDesc &kd, bool upper, bool first) {
+            if (upper) {
 #pragma unroll
-                    for (int n = 0; n < 16; n++)
-                        mma_bf16_ss_warp(dS, qd.at((n >> 2) * 1024 + 2 * (n & 3)), kd.at((n >> 2) * 64 + 2 * (n & 3)), idS,
-                                    !first || n > 0);
-                } else {
+                for (int n = 0; n < 16; n++)
+                    mma_bf16_ss_warp(dS, qd.at((n >> 2) * 1024 + 2 * (n & 3)), kd.at((n >> 2) * 64 + 2 * (n & 3)), idS,
+                                !first || n > 0);
+            } else {
 #pragma unroll
-                    for (int n = 0; n < 16; n++)
-                        mma_bf16_ts_warp(dS, tm + kColQ + 8 * n, kd.at((n >> 2) * 64 + 2 * (n & 3)), idS, !first || n > 0);
+                for (int n = 0; n < 16; n++)
+                    mma_bf16_ts_warp(dS, tm + kColQ + 8 * n, kd.at((n >> 2) * 64 + 2 * (n & 3)), idS, !first || n > 0);
+            }
+        };
+        for (; ok && cur.next(p, w, sg); k++)
+            for (int t = sg.s0; t < sg.s1; t++, g++) {
+                const int st = g & 1;
+                // (Q in tensor memory, then in shared memory: its barrier's odd phase)
+                if (t == sg.s0 && (!wait(qready, k & 1) || !wait(qland, 1))) break;
+                if (g > 0 && !wait(sfree, (g - 1) & 1)) break;
+                if (!wait(&kfull[2 * st], (g >> 1) & 1)) break;
+                tc_fence_after();
+                const SDesc kd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage, 16, kGroupA)));
+                four(kd, half == 0, true);
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    const uint64_t b = kd.at(4 * 64 + 2 * u);
+                    mma_bf16_ts_warp(dS, tm + kColR + 8 * u, b, idS, 1u);
+                    mma_bf16_ts_warp(dS, tm + kColR + 32 + 8 * u, b, idS, 1u);
                 }
-            };
-            for (; ok && cur.next(p, w, sg); k++)
-                for (int t = sg.s0; t < sg.s1; t++, g++) {
-                    const int st = g & 1;
-                    // (Q in tensor memory, then in shared memory: its barrier's odd phase)
-                    if (t == sg.s0 && (!wait(qready, k & 1) || !wait(qland, 1))) break;
-                    if (g > 0 && !wait(sfree, (g - 1) & 1)) break;
-                    if (!wait(&kfull[2 * st], (g >> 1) & 1)) break;
-                    tc_fence_after();
-                    const SDesc kd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage, 16, kGroupA)));
-                    four(kd, half == 0, true);
-#pragma unroll
-                    for (int u = 0; u < 4; u++) {
-                        const uint64_t b = kd.at(4 * 64 + 2 * u);
-                        mma_bf16_ts_warp(dS, tm + kColR + 8 * u, b, idS, 1u);
-                        mma_bf16_ts_warp(dS, tm + kColR + 32 + 8 * u, b, idS, 1u);
-                    }
-                    mma_commit_warp(&kempty[2 * st]);
-                    if (!wait(&kfull[2 * st + 1], (g >> 1) & 1)) break;
-                    tc_fence_after();
-                    four(uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 16, kGroupB))), half != 0, false);
-                    if (t + 1 == sg.s1) mma_commit_warp(qfree);
-                    mma_commit_warp(sfull);
-                }
-        }
+                mma_commit_warp(&kempty[2 * st]);
+                if (!wait(&kfull[2 * st + 1], (g >> 1) & 1)) break;
+                tc_fence_after();
+                four(uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 16, kGroupB))), half != 0, false);
+                if (t + 1 == sg.s1) mma_commit_warp(qfree);
+                mma_commit_warp(sfull);
+            }
     } else if (warp == kWarpM + 1) {
         // ------------------------------------------------------- O += P V
-        {
-            const uint32_t idO = idesc_bf16(128, 256, 1), tm = uniform(tmem);
-            const SDesc pd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oP), 16, 1024)));
-            uint32_t g = 0, k = 0;
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && warp_all(mbar_wait(bar, parity, abort_flag, wlim)); };
-            for (; ok && cur.next(p, w, sg); k++)
-                for (int t = sg.s0; t < sg.s1; t++, g++) {
-                    const int st = g & 1;
-                    if (!wait(pready, g & 1) || (t == sg.s0 && k > 0 && !wait(ofree, (k - 1) & 1))) break;
-                    tc_fence_after();
-                    const SDesc vd =
-                        uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 1024, kGroupB)));
+        const uint32_t idO = idesc_bf16(128, 256, 1), tm = uniform(tmem);
+        const SDesc pd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oP), 16, 1024)));
+        uint32_t g = 0, k = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return ok = ok && warp_all(mbar_wait(bar, parity, abort_flag, wlim));
+        };
+        for (; ok && cur.next(p, w, sg); k++)
+            for (int t = sg.s0; t < sg.s1; t++, g++) {
+                const int st = g & 1;
+                if (!wait(pready, g & 1) || (t == sg.s0 && k > 0 && !wait(ofree, (k - 1) & 1))) break;
+                tc_fence_after();
+                const SDesc vd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 1024, kGroupB)));
 #pragma unroll
-                    for (int u = 0; u < 4; u++)
-                        mma_bf16_ss_warp(tm + kColO, pd.at(2 * u), vd.at(2 * (kGroupB / 16) * u), idO, t != sg.s0 || u > 0 ? 1u : 0u);
-                    mma_commit_warp(&kempty[2 * st + 1]);
-                    mma_commit_warp(pvdone);
-                }
-        }
+                for (int u = 0; u < 4; u++)
+                    mma_bf16_ss_warp(tm + kColO, pd.at(2 * u), vd.at(2 * (kGroupB / 16) * u), idO, t != sg.s0 || u > 0 ? 1u : 0u);
+                mma_commit_warp(&kempty[2 * st + 1]);
+                mma_commit_warp(pvdone);
+            }
     } else {
         // -------------------------------------------------------- softmax
         const int q4 = warp & 3, hf = warp >> 2, r = q4 * 32 + lane;

@@ -66,6 +66,7 @@ __device__ __forceinline__ void mma_commit_warp(uint64_t *bar) {
 // The value of lane 0, known to be the same in all lanes.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ SDesc uniform(const SDesc &d) { return SDesc{uniform(d.lo), uniform(d.hi)}; }
+__device__ __forceinline__ SDesc sdesc_plus(const SDesc &d, uint32_t bytes) { return SDesc{d.lo + bytes / 16, d.hi}; }
 // 4-D tiled TMA load (no multicast) completing on bar's transaction count.
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, uint64_t *bar, int x, int y, int z,
                                             int w) {

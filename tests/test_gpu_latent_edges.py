@@ -21,7 +21,8 @@ def lib():
 
 
 def _runs_out(call):
-    """call (returning its workspace) with waits of 1 ns: the device error, and only once."""
+    """call (returning its workspace) with waits of 1 ns: the device error, and only once. (A wait looks at the time
+    after 64 polls of up to a few microseconds each; the sizes here make some wait for longer.)"""
     prev = capi.set_wait_limit_ns(1)
     try:
         ws = call()
@@ -41,13 +42,13 @@ def _close(a, b):
 
 def test_draft_waits_run_out_and_the_context_recovers():
     S, W = 300, 128
-    t = make(5, 1, S, 40, 64, 512, 64, "bf16")
+    t = make(5, 1, S, 300, 64, 512, 64, "bf16")
     before = run(t, S, W)
     d = {k: v.cuda() for k, v in t.items()}
     _runs_out(lambda: capi.latent_attn_fwd(d["q"], d["c"], d["kr"], d["an"], d["kp"], S, W)[2])
 
     def bwd():
-        ws = capi.alloc_latent_workspace(capi.latent_problem(1, 64, S, 40, W), "cuda")
+        ws = capi.alloc_latent_workspace(capi.latent_problem(1, 64, S, 300, W), "cuda")
         capi.latent_attn_bwd(d["q"], d["c"], d["kr"], d["an"], d["kp"], before["lse"], d["dout"], S, W, workspace=ws)
         return ws
 
@@ -59,13 +60,15 @@ def test_draft_waits_run_out_and_the_context_recovers():
         _close(before[k], after[k])
 
 
-@pytest.mark.parametrize("kind", ["bf16", "fp8"])
-@pytest.mark.parametrize("name", ["long", "short"])
+@pytest.mark.parametrize("name,kind", [("long", "bf16"), ("short", "bf16"), ("short", "fp8")])
 def test_paged_waits_run_out_and_the_context_recovers(name, kind):
-    q_lens, kv_lens, window = ([1, 4], [3000, 2500], 0) if name == "long" else ([5] * 64, [200] * 64, 128)
-    n_pages, table, qs, kv = plan(71, q_lens, kv_lens, 16)
-    cache, _, _ = filled(72, kind, n_pages, 16, 512, 64)
-    q = torch.randn(sum(q_lens), 64, 576, generator=torch.Generator().manual_seed(73)).to(torch.bfloat16).cuda()
+    n_seq, q_len, kv_len, window = (2, 20, 40000, 0) if name == "long" else (300, 5, 200, 128)
+    cache, _, _ = filled(72, kind, 64, 16, 512, 64)
+    g = torch.Generator().manual_seed(73)
+    table = torch.randint(0, 64, (n_seq, -(-kv_len // 16)), generator=g, dtype=torch.int32)
+    qs = torch.arange(n_seq + 1, dtype=torch.int32) * q_len
+    kv = torch.full((n_seq,), kv_len, dtype=torch.int32)
+    q = torch.randn(n_seq * q_len, 64, 576, generator=g).to(torch.bfloat16).cuda()
     args = (q, cache, table.cuda(), qs.cuda(), kv.cuda())
     o, lse, ws = capi.latent_attn_paged(*args, window=window)
     capi.get_error(ws)

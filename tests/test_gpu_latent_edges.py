@@ -170,3 +170,39 @@ def test_repeated_tokens_or_heads_are_refused():
     o = torch.zeros(1, 1, 512, dtype=torch.bfloat16, device="cuda").expand(2, 8, 512)
     with pytest.raises(ValueError):
         capi.latent_attn_paged(q, cache, table, qs, kv, out=(o, torch.zeros(2, 8, device="cuda")))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
+def test_nothing_to_do(kind):
+    """No tokens, no sequences, no pages: calls that write what they have to and nothing else."""
+    dt = torch.float32 if kind == "f32" else torch.bfloat16
+    cache, _, _ = filled(111, kind, 3, 8, 512, 64)
+    before = cache.clone()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    none = torch.empty(0, 64, 576, dtype=dt, device="cuda")
+    o, lse, ws = capi.latent_attn_paged(none, cache, torch.zeros(2, 3, **i32), torch.zeros(3, **i32),
+                                        torch.full((2,), 20, **i32))
+    capi.get_error(ws)
+    assert o.shape == (0, 64, 512) and lse.shape == (0, 64)
+    q = torch.randn(4, 64, 576, device="cuda").to(dt)
+    out = (torch.full((4, 64, 512), 3.0, dtype=dt, device="cuda"), torch.full((4, 64), 2.0, device="cuda"))
+    _, _, ws = capi.latent_attn_paged(q, cache, torch.zeros(0, 3, **i32), torch.zeros(1, **i32),
+                                      torch.zeros(0, **i32), out=out)
+    capi.get_error(ws)
+    assert bool((out[0] == 3).all()) and bool((out[1] == 2).all())
+    # sequences without keys: zero rows
+    no_pages = torch.empty((0, 8) + cache.shape[2:], dtype=cache.dtype, device="cuda")
+    _, _, ws = capi.latent_attn_paged(q, no_pages, torch.zeros(2, 0, **i32), torch.tensor([0, 1, 4], **i32),
+                                      torch.zeros(2, **i32), out=out)
+    capi.get_error(ws)
+    assert torch.count_nonzero(out[0]) == 0 and torch.isneginf(out[1]).all()
+    # no rows, and rows of slots out of range
+    empty = torch.empty(0, dtype=torch.int64, device="cuda")
+    capi.latent_cache_write(cache, none[:, 0, :512].contiguous(), none[:, 0, 512:].contiguous(), empty.int(), empty)
+    slots = torch.tensor([-1, 24, 1 << 40, -(1 << 40)], device="cuda")
+    capi.latent_cache_write(cache, q[:, 0, :512].contiguous(), q[:, 0, 512:].contiguous(), slots.int(), slots)
+    assert torch.equal(cache, before)
+    c, kr = capi.latent_cache_read(cache, empty)
+    assert c.shape == (0, 512) and kr.shape == (0, 64)
+    c, kr = capi.latent_cache_read(cache, slots)
+    assert torch.count_nonzero(c) == 0 and torch.count_nonzero(kr) == 0

@@ -270,10 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0), idQ = idesc_bf16(128, 64, 1);
         const uint32_t idK = idesc_bf16_ab(128, 64, 1, 1), idD = idesc_bf16_ab(128, 32, 1, 0);
         const int ksc = p.ctxpad / 16, ksr = (p.hp * kBlock + 15) / 16;
-        const SDesc dsr = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDS), 16, 1024)));         // rows x keys
         const SDesc dst = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDS), kSlot, 1024)));      // keys x rows
         const SDesc pt = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oPr), kSlot, 1024)));
-        const SDesc dda = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 32 * 128, 1024)));   // rows x draft keys
         const SDesc ddb = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oDD), 16, 1024)));         // draft keys x rows
         // slots of keys, and of Q and dO, as rows x columns and transposed
         const SDesc sk = uniform(sdesc_split(sdesc_sw128(smem_u32(sm + oK), 16, 1024)));
@@ -307,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; ok && cu.next(p, cur); k++) {
             const uint32_t kn = k * (2 * kSlices + 1), qn = k * 2 * kSlices;  // the tile's first copies
             if (who == 0) {
-                // S and dP of the tile before are read
-                if (k > 0 && !wait(pds, (k - 1) & 1)) break;
+                // S and dP of the tile before are read, and dS, over S, by the products of dq
+                if (k > 0 && (!wait(pds, (k - 1) & 1) || !wait(&done[0], (k - 1) & 1))) break;
 #pragma unroll 1
                 for (int c = 0; c < kSlices; c++) {
                     const uint32_t ks = take_k(1, kn + c), qs = take_q(1, qn + c);
@@ -350,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (unrolled: a product of 64 columns takes 50 cycles, a step of a rolled loop 90)
 #pragma unroll
                     for (int s = 0; s < 8; s++)
-                        if (s < ksc) mma_bf16_ss_warp(d, dsr.at((s >> 2) * (kSlot / 16) + (s & 3) * 2), kv.at(128 * s), idQ, s > 0);
-                    mma_bf16_ss_warp(d, dda.at(0), kv.at(p.ctxpad * 8), idK, ksc > 0);
+                        if (s < ksc) mma_bf16_ts_warp(d, tm + kColS + 8 * s, kv.at(128 * s), idQ, s > 0);
+                    mma_bf16_ts_warp(d, tm + kColS + p.ctxpad / 2, kv.at(p.ctxpad * 8), idQ, ksc > 0);
                     mma_commit_warp(&kempty[ks]);
                     if (c == kSlices - 1) mma_commit_warp(&done[0]);
                     mma_commit_warp(qcfull);  // last: nothing is in flight once its reader has it
@@ -441,10 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float D = (D4[0] + D4[1]) + (D4[2] + D4[3]);
             xd[hf * 128 + r] = D;
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&lbar[q4]);
             ok = warp_all(mbar_wait(&lbar[q4], k & 1, abort_flag, wlim));
             if (!ok) break;
+            tc_fence_after();
             D += xd[(hf ^ 1) * 128 + r];
             // the products of the tile before have read P and dS
             if (k > 0) {
@@ -463,20 +463,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 32; x++) g[x] = (in[cc] >> x) & 1 ? g[x] : D;
                     }
+                    // dS twice: rows x keys over S in tensor memory (both halves have read it),
+                    // for dq, and in shared memory, read transposed, for dk
+                    uint32_t b[16];
+#pragma unroll
+                    for (int x = 0; x < 16; x++)
+                        b[x] = pack_bf16x2(P[32 * cc + 2 * x] * (g[2 * x] - D) * p.scale,
+                                           P[32 * cc + 2 * x + 1] * (g[2 * x + 1] - D) * p.scale);
+                    tmem_st16u(trow + kColS + 32 * hf + 16 * cc, b);
                     if (r < kRows) {
 #pragma unroll
                         for (int u = 0; u < 4; u++) {
-                            uint32_t a[4], b[4];
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const int x = 8 * u + 2 * e;
-                                const float p0 = P[32 * cc + x], p1 = P[32 * cc + x + 1];
-                                a[e] = pack_bf16x2(p0, p1);
-                                b[e] = pack_bf16x2(p0 * (g[x] - D) * p.scale, p1 * (g[x + 1] - D) * p.scale);
-                            }
+                            const float *pp = &P[32 * cc + 8 * u];
                             const uint32_t at = hf * kSlot + sw128(r, 4 * cc + u);
-                            *reinterpret_cast<uint4 *>(sm + oPr + at) = make_uint4(a[0], a[1], a[2], a[3]);
-                            *reinterpret_cast<uint4 *>(sm + oDS + at) = make_uint4(b[0], b[1], b[2], b[3]);
+                            *reinterpret_cast<uint4 *>(sm + oPr + at) =
+                                make_uint4(pack_bf16x2(pp[0], pp[1]), pack_bf16x2(pp[2], pp[3]), pack_bf16x2(pp[4], pp[5]),
+                                           pack_bf16x2(pp[6], pp[7]));
+                            *reinterpret_cast<uint4 *>(sm + oDS + at) =
+                                make_uint4(b[4 * u], b[4 * u + 1], b[4 * u + 2], b[4 * u + 3]);
                         }
                     }
                 }
@@ -485,13 +489,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // draft keys: one bf16 to each of their rows
                 uint8_t *dd = sm + oDD + (r >> 6) * (32 * 128) + (r & 7) * 2;
                 const int u = (r & 63) >> 3;
+                float ds[8];
+#pragma unroll
+                for (int x = 0; x < 8; x++) ds[x] = x < kBlock && live ? pd[x] * (gd[x] - D) * p.scale : 0.f;
+                uint32_t b[8];
+#pragma unroll
+                for (int x = 0; x < 8; x++) b[x] = x < 4 ? pack_bf16x2(ds[2 * (x & 3)], ds[2 * (x & 3) + 1]) : 0u;
+                tmem_st8u(trow + kColS + p.ctxpad / 2, b);
 #pragma unroll
                 for (int x = 0; x < kBlock; x++) {
-                    *reinterpret_cast<__nv_bfloat16 *>(dd + sw128(x, u)) =
-                        __float2bfloat16_rn(live ? pd[x] * (gd[x] - D) * p.scale : 0.f);
+                    *reinterpret_cast<__nv_bfloat16 *>(dd + sw128(x, u)) = __float2bfloat16_rn(ds[x]);
                     *reinterpret_cast<__nv_bfloat16 *>(dd + sw128(16 + x, u)) = __float2bfloat16_rn(pd[x]);
                 }
             }
+            tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();

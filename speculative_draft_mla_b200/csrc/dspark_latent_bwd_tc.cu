@@ -10,9 +10,9 @@
 //   dd_c = Q_c^T dS_d, dO_c^T P_d       columns x draft keys (one product: the two
 //                                       column sets are its 128 rows, the two key
 //                                       sets its 32 columns)
-// P and dS go through shared memory, where rows-by-keys tiles serve as they are
-// (dS K) and transposed (dS^T Q). Key gradients of all heads and of the blocks
-// whose windows overlap meet in an fp32 accumulator [B, L, 576] by vector
+// P and dS go through shared memory, where rows-by-keys tiles are read transposed
+// (dS^T Q), and dS, for dS K, to tensor memory besides. Key gradients of all heads and of the blocks
+// whose windows overlap meet in an fp32 accumulator [B, L, 576] by
 // reductions; the last launch turns its rope part back and rounds.
 //
 // The 132 x 576 fp32 key gradients of a block (304 KB) fit neither tensor
@@ -21,11 +21,14 @@
 // twice per tile: for S and dP, and, from L2, for the gradients. (Gradients of a
 // tile interleaved with S and dP of the next share the keys' slices, but need
 // two slots of Q and dO a slice, and with the three that fit the copies' latency
-// is exposed: 4500 cycles a slice against 2700.) What bounds it: shared
-// memory while gradients are formed (of 2900 cycles a slice, the operands of its
-// products take 1440 at 128 bytes a cycle, the copies in 360, dq and dk on their way
-// out 740), and the copies' latency while S and dP are (1900 a slice, 16000 a
-// tile of 44000).
+// is exposed: 4500 cycles a slice against 2700.)
+//
+// What bounds it (S = 4096, N = 512, B = 4, a tenth padding: 1010 us with its
+// preparation, 42000 cycles a tile): the gradients, 26000, whose 30 short products a
+// slice take 1500 cycles by their shared-memory operands beside 1100 of copies in
+// and results out; S and dP, 15000, by the latency of copies that three slots
+// hide in part; the softmax between, 4400. DRAM moves little more than it must
+// (1.53 GB read, 0.74 GB written; L2 serves the second reads).
 //
 // Sums of key gradients are fp32 in whatever order the tiles finish: two runs
 // may differ in the last bits before the rounding to bf16. P and dS are bf16
@@ -33,10 +36,11 @@
 // rope slices of Q and K are hi + lo of two bf16 in S, as in the forward, and Q's
 // in its product with dS: one bf16 would nearly double the error of dkr.
 //
-// TMEM: S 0..143, dP 144..287, dq 288..351, dk 352..415 / 416..479, dd 480..511.
+// TMEM: S 0..143 (then dS, bf16), dP 144..287, dq 288..351, dk 352..415 / 416..479, dd 480..511.
 // Warps 0-7 softmax (warps w and w + 4 share 32 rows, 64 context keys each);
 // 0-3 then take dq and dd, 4-7 dk; 8 loads keys, 9 Q and dO, 10 - 12 issue the
-// MMAs, 13 stores dq. Every wait is bounded.
+// MMAs (as whole warps: 1010 us, one lane of each 1084), 13 stores dq. Every wait
+// is bounded.
 #include <algorithm>
 
 #include "dspark_latent_tc.cuh"
@@ -263,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kWarpM) {
         // -------------------------------------------------------- MMAs
-        // Three issuers (one thread of each warp), as a single thread issuing all
-        // products was slower than the products: 0 S and dP, 1 dq, 2 dk and dd.
+        // Three issuers, as one issuing all products was slower than the products: 0 S
+        // and dP, 1 dq, 2 dk and dd (four, dd apart: 1141 us against 1058).
         const int who = (int)uniform((uint32_t)(warp - kWarpM));
         const uint32_t tm = uniform(tmem);
         const uint32_t idS = idesc_bf16(128, p.ctxpad + 16, 0), idQ = idesc_bf16(128, 64, 1);
@@ -654,7 +658,7 @@ bool make_acc_map(CUtensorMap *m, float *acc, uint64_t L, uint64_t B) {
 }
 
 // The queries' rope slices turned to their positions, hi then lo, and the
-// key gradients' accumulators cleared.
+// key gradients' accumulators cleared: 313 MB at S = 4096, N = 512, B = 4, about 50 us.
 __global__ void __launch_bounds__(256) k_lat_bwd_prep(const __nv_bfloat16 *__restrict__ q,
                                                       const int32_t *__restrict__ anchors,
                                                       const float2 *__restrict__ tab, __nv_bfloat16 *__restrict__ out,

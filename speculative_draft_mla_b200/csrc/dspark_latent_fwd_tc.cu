@@ -11,7 +11,8 @@
 //
 // What bounds it is the stream of Q in (1152 B a row) and O out (1024 B a row):
 // at S = 8192, N = 512, B = 2 they are 0.71 GB of the 0.74 GB that have to move,
-// 113 us at the measured copy rate, against 58 us of tensor work. So Q comes
+// 113 us at the measured copy rate, against 58 us of tensor work; measured 177 us
+// (S = 2048, N = 128, B = 1: 35.5, of which 32 are one round of 2 or 3 tiles). So Q comes
 // in 64-column slices through a ring of three, feeding S = Q K^T slice by
 // slice, and O leaves in eight 64-column products P V through two accumulators;
 // S is double-buffered, so the loads of one tile go on while the tile before it

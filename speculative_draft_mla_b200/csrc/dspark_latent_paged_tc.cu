@@ -24,9 +24,12 @@
 // half's values, the rope keys) are free for the step after next once S is formed,
 // the other four once O is.
 //
-// What bounds it: long contexts, the tensor work (40 products of 64 keys take 50
-// cycles each, 4 of 256 columns 134: 2500 cycles a step) and the softmax beside
-// it; few keys, the latency of the launches, of Q and of a step.
+// What bounds it: long contexts (16 sequences of 6 tokens over up to 16384 keys,
+// 244 us), the issue and the tensor work of a step, 3000 of its 4000 cycles (40
+// products of 64 keys, 50 cycles each where nothing else runs, 4 of 256 columns,
+// 134; issued by one lane, 268 us), and the way from S to the softmax and
+// back; few keys, the latency of the launches, of Q and of a step (one token over
+// 8192 keys, 33 us: plan 6, this kernel 13, join 8).
 //
 // The query's turned rope slice is split as hi + lo of two bf16 (the cache's
 // rope keys are exact bf16 operands), so scores and LSE keep 2^-16.

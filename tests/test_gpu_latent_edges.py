@@ -206,3 +206,33 @@ def test_nothing_to_do(kind):
     assert c.shape == (0, 512) and kr.shape == (0, 64)
     c, kr = capi.latent_cache_read(cache, slots)
     assert torch.count_nonzero(c) == 0 and torch.count_nonzero(kr) == 0
+
+
+@pytest.mark.parametrize("n_h", [100, 128, 129, 256])
+@pytest.mark.parametrize("kind,window", [("bf16", 0), ("fp8", 90)])
+def test_head_counts_around_a_tile(n_h, kind, window):
+    """Heads that just fill a tile of rows, leave some, need one of the next chunk, or fill two."""
+    q_lens, kv_lens, page = [2, 1], [170, 60], 16
+    n_pages, table, qs, kv = plan(121, q_lens, kv_lens, page)
+    cache, lat, rope = filled(122, kind, n_pages, page, 512, 64)
+    q = torch.randn(3, n_h, 576, generator=torch.Generator().manual_seed(123)).to(torch.bfloat16)
+    val, err = reference(q.double().numpy(), lat, rope, table.numpy(), qs.numpy(), kv.numpy(), page,
+                         capi.LATENT_SCALE, True, window, True)
+    o, lse, ws = capi.latent_attn_paged(q.cuda(), cache, table.cuda(), qs.cuda(), kv.cuda(), window=window)
+    capi.get_error(ws)
+    lp.check("o", o, val["o"], err["o"])
+    lp.check("lse", lse, val["lse"], err["lse"])
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,N", [(0, 3), (2, 0)])
+def test_empty_batches(B, N, dt):
+    S, n_h = 20, 64
+    q = torch.zeros(B, n_h, 5 * N, 576, dtype=dt, device="cuda")
+    c, kr = (torch.ones(B, S + 5 * N, d, dtype=dt, device="cuda") for d in (512, 64))
+    an, kp = (torch.ones(B, N, dtype=t, device="cuda") for t in (torch.int32, torch.uint8))
+    o, lse, ws = capi.latent_attn_fwd(q, c, kr, an, kp, S, 8)
+    capi.get_error(ws)
+    dq, dc, dkr = capi.latent_attn_bwd(q, c, kr, an, kp, lse, o, S, 8, workspace=ws)
+    capi.get_error(ws)
+    assert dq.shape == q.shape and torch.count_nonzero(dc) == 0 and torch.count_nonzero(dkr) == 0

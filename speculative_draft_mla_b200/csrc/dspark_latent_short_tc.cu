@@ -16,14 +16,16 @@
 // that is not finite and not its own (0 x NaN) is evaluated again by its warp.
 //
 // 128 sequences of 5 tokens, 64 heads, window 128, 8-bit rows: 44 us, one item to an
-// SM, so that the latency of the keys and of the first tile is in the open.
+// SM, so that the latency of the keys and of the first tile is in the open, and that
+// of code not yet in the instruction cache: loops over keys that were unrolled more
+// made it 60.
 // What bounds it beyond: Q in (1152 B a row) and O out (1024 B); per tile 36 products of
 // 144 keys (80 cycles) and 72 of 64 columns (50).
 //
 // TMEM: S 0..143 / 144..287 (P over its own S columns), rope query hi, lo
 // 288..351, O 352..415 / 416..479.
 // Warps: 0-3 and 4-7 softmax and output of even and odd tiles (thread = row);
-// 8-11 keys, and the queries' rope slices; 12 loads Q slices, 13 and 14 issue the
+// 8-11 keys (of a CTA's first item 0-11), and the queries' rope slices; 12 loads Q slices, 13 and 14 issue the
 // products of S and of O. Every wait is bounded.
 #include <algorithm>
 
@@ -42,7 +44,7 @@ constexpr int oQ = 9 * kKSlice, oBar = oQ + kQSlots * kQSlot;
 constexpr int kSmem = oBar + 512 + 1024;
 static_assert(kSmem <= 232448 && kKSlice % 1024 == 0, "shared memory");
 constexpr uint32_t kColS = 0, kColR = 2 * kKeys, kColO = kColR + 64;
-constexpr int kWarpA = 8, kWarpQ = 12, kWarpM = 13, kThreads = 15 * 32;
+constexpr int kLoaders = 12, kWarpA = 8, kWarpQ = 12, kWarpM = 13, kThreads = 15 * 32;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // An item's sequence and tiles.
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t wlim = p.wait_ns;
 
     if (threadIdx.x == 0) {
-        mbar_init(kfull, 4);
+        mbar_init(kfull, kLoaders);
         mbar_init(kempty, 1);
         for (int i = 0; i < 2 * kQSlots; i++) mbar_init(&qfull[i], 1);
         for (int i = 0; i < 2; i++) {
@@ -134,6 +136,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t issued_q = 0;
     Item it;
 
+    // An item's keys, by some of warps: groups first, first + warps, ... of 8 slots, two at a time.
+    const uint8_t *cache = (const uint8_t *)p.cache;
+    const auto load_keys = [&](const Item &it, int first, int warps) {
+        for (int g0 = first; g0 < it.ncol / 8; g0 += 2 * warps) {
+            long long off[2];
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+                const int slot = 8 * (g0 + warps * y) + (lane & 7), key = it.lo + slot;
+                long long at = -1;
+                if (slot < it.ncol && key < it.hi) {
+                    at = key_slot(p, it.seq, key);
+                    if (at < 0 && lane < 8) atomicOr(p.err, kErrPage);
+                }
+                const uint32_t valid = __ballot_sync(0xffffffffu, at >= 0) & 0xffu;
+                if (lane == 0 && slot < it.ncol) reinterpret_cast<volatile uint8_t *>(kmask)[g0 + warps * y] = (uint8_t)valid;
+                off[y] = at >= 0 ? at * (long long)p.row_bytes : -1;
+            }
+            if constexpr (KIND == DSPARK_CACHE_BF16) {
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    if (8 * (g0 + warps * y) >= it.ncol) continue;
+#pragma unroll
+                    for (int e = 0; e < 18; e++) {
+                        const int x = lane + 32 * e, row = x / 72, ch = x % 72;
+                        const long long o = __shfl_sync(0xffffffffu, off[y], row);
+                        cp16(smem_u32(sm) + (ch >> 3) * kKSlice + sw128(8 * (g0 + warps * y) + row, ch & 7),
+                             cache + (o >= 0 ? o + ch * 16 : 0), o >= 0);
+                    }
+                }
+            } else {
+                uint4 x[2][8];
+                float4 sc[2];
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    if (8 * (g0 + warps * y) >= it.ncol) continue;
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {  // the rope slice as it is
+                        const int row = 4 * e + (lane >> 3), ch = lane & 7;
+                        const long long o = __shfl_sync(0xffffffffu, off[y], row);
+                        cp16(smem_u32(sm) + 8 * kKSlice + sw128(8 * (g0 + warps * y) + row, ch),
+                             cache + (o >= 0 ? o + kDL + ch * 16 : 0), o >= 0);
+                    }
+                    const long long o = __shfl_sync(0xffffffffu, off[y], lane >> 2);
+                    const uint8_t *row = cache + (o >= 0 ? o : 0);
+                    sc[y] = o >= 0 ? __ldg(reinterpret_cast<const float4 *>(row + kDL + 2 * kDR))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int s = 0; s < 8; s++)
+                        x[y][s] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * s + 16 * (lane & 3)))
+                                         : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    if (8 * (g0 + warps * y) >= it.ncol) continue;
+                    const int row = 8 * (g0 + warps * y) + (lane >> 2);
+#pragma unroll
+                    for (int s = 0; s < 8; s++) {
+                        const float f = s < 2 ? sc[y].x : s < 4 ? sc[y].y : s < 6 ? sc[y].z : sc[y].w;
+                        const uint4 v = x[y][s];
+                        *reinterpret_cast<uint4 *>(sm + s * kKSlice + sw128(row, 2 * (lane & 3))) =
+                            make_uint4(fp8x2_bf16(v.x, f), fp8x2_bf16(v.x >> 16, f), fp8x2_bf16(v.y, f),
+                                       fp8x2_bf16(v.y >> 16, f));
+                        *reinterpret_cast<uint4 *>(sm + s * kKSlice + sw128(row, 2 * (lane & 3) + 1)) =
+                            make_uint4(fp8x2_bf16(v.z, f), fp8x2_bf16(v.z >> 16, f), fp8x2_bf16(v.w, f),
+                                       fp8x2_bf16(v.w >> 16, f));
+                    }
+                }
+            }
+        }
+        cp_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+    // The first item's keys by the warps that would wait for them too (128 sequences
+    // of 5 tokens, 8-bit rows: 43.5 us with four warps, 40.7).
+    if (warp < kLoaders && item_at(p, w, parts, blockIdx.x, it) && it.t0 < it.t1) {
+        load_keys(it, warp, kLoaders);
+        if (lane == 0) mbar_arrive(kfull);
+    }
+
     if (warp == kWarpQ) {
         // ------------------------------------------------------ Q slices
         if (lane == 0) {
@@ -157,84 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------ keys; rope slices of the queries -> TMEM
         const int wr = warp - kWarpA, r = wr * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(wr * 32) << 16) + kColR;
-        const uint8_t *cache = (const uint8_t *)p.cache;
         uint32_t k = 0, n = 0;  // items, tiles
         bool ok = true;
         for (int i = blockIdx.x; ok && item_at(p, w, parts, i, it); i += G) {
             if (it.t0 == it.t1) continue;
             if (k > 0) ok = warp_all(mbar_wait(kempty, (k - 1) & 1, abort_flag, wlim));
             if (!ok) break;
-            // warp wr takes groups wr, wr + 4, ... of 8 slots, two groups at a time
-            for (int g0 = wr; g0 < it.ncol / 8; g0 += 8) {
-                long long off[2];
-#pragma unroll
-                for (int y = 0; y < 2; y++) {
-                    const int slot = 8 * (g0 + 4 * y) + (lane & 7), key = it.lo + slot;
-                    long long at = -1;
-                    if (slot < it.ncol && key < it.hi) {
-                        at = key_slot(p, it.seq, key);
-                        if (at < 0 && lane < 8) atomicOr(p.err, kErrPage);
-                    }
-                    const uint32_t valid = __ballot_sync(0xffffffffu, at >= 0) & 0xffu;
-                    if (lane == 0 && slot < it.ncol) reinterpret_cast<volatile uint8_t *>(kmask)[g0 + 4 * y] = (uint8_t)valid;
-                    off[y] = at >= 0 ? at * (long long)p.row_bytes : -1;
-                }
-                if constexpr (KIND == DSPARK_CACHE_BF16) {
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {
-                        if (8 * (g0 + 4 * y) >= it.ncol) continue;
-#pragma unroll
-                        for (int e = 0; e < 18; e++) {
-                            const int x = lane + 32 * e, row = x / 72, ch = x % 72;
-                            const long long o = __shfl_sync(0xffffffffu, off[y], row);
-                            cp16(smem_u32(sm) + (ch >> 3) * kKSlice + sw128(8 * (g0 + 4 * y) + row, ch & 7),
-                                 cache + (o >= 0 ? o + ch * 16 : 0), o >= 0);
-                        }
-                    }
-                } else {
-                    uint4 x[2][8];
-                    float4 sc[2];
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {
-                        if (8 * (g0 + 4 * y) >= it.ncol) continue;
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {  // the rope slice as it is
-                            const int row = 4 * e + (lane >> 3), ch = lane & 7;
-                            const long long o = __shfl_sync(0xffffffffu, off[y], row);
-                            cp16(smem_u32(sm) + 8 * kKSlice + sw128(8 * (g0 + 4 * y) + row, ch),
-                                 cache + (o >= 0 ? o + kDL + ch * 16 : 0), o >= 0);
-                        }
-                        const long long o = __shfl_sync(0xffffffffu, off[y], lane >> 2);
-                        const uint8_t *row = cache + (o >= 0 ? o : 0);
-                        sc[y] = o >= 0 ? __ldg(reinterpret_cast<const float4 *>(row + kDL + 2 * kDR))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int s = 0; s < 8; s++)
-                            x[y][s] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * s + 16 * (lane & 3)))
-                                             : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {
-                        if (8 * (g0 + 4 * y) >= it.ncol) continue;
-                        const int row = 8 * (g0 + 4 * y) + (lane >> 2);
-#pragma unroll
-                        for (int s = 0; s < 8; s++) {
-                            const float f = s < 2 ? sc[y].x : s < 4 ? sc[y].y : s < 6 ? sc[y].z : sc[y].w;
-                            const uint4 v = x[y][s];
-                            *reinterpret_cast<uint4 *>(sm + s * kKSlice + sw128(row, 2 * (lane & 3))) =
-                                make_uint4(fp8x2_bf16(v.x, f), fp8x2_bf16(v.x >> 16, f), fp8x2_bf16(v.y, f),
-                                           fp8x2_bf16(v.y >> 16, f));
-                            *reinterpret_cast<uint4 *>(sm + s * kKSlice + sw128(row, 2 * (lane & 3) + 1)) =
-                                make_uint4(fp8x2_bf16(v.z, f), fp8x2_bf16(v.z >> 16, f), fp8x2_bf16(v.w, f),
-                                           fp8x2_bf16(v.w >> 16, f));
-                        }
-                    }
-                }
+            if (i != (int)blockIdx.x) {
+                load_keys(it, wr, 4);
+                if (lane < kLoaders / 4) mbar_arrive(kfull);
             }
-            cp_wait_all();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(kfull);
             k++;
             for (int t = it.t0; ok && t < it.t1; t++, n++) {
                 const RowOf o(p, w, it, t, r);

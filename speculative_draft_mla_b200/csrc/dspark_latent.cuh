@@ -71,10 +71,19 @@ inline LatWs lat_view(const Prob &p, void *ws) {
     return w;
 }
 
-// turned rope keys; with pad != NULL, the padding blocks' rows too (t[0] per
-// head, t[1] and t[2] shared by the heads)
+// What the tensor-core backward needs beside the turned rope keys.
+constexpr int kTcDL = 512, kTcDR = 64;  // widths of the tensor-core kernels
+struct BwdPrep {
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;  // [rows, 2, 64]: turned rope slices, hi, lo
+    float4 *acc;         // cleared
+    size_t rows, acc4;
+};
+
+// turned rope keys; with pad != NULL, the padding blocks' rows of t[0] too; with
+// bwd, BwdPrep for the queries q (tensor-core widths, bf16)
 cudaError_t launch_lat_prep(const Prob &p, const void *kr, const int32_t *anchors, const uint8_t *keep,
-                            const PadRows *pad, bool tc, const LatWs &ws, cudaStream_t st);
+                            const PadRows *pad, bool tc, bool bwd, const void *q, const LatWs &ws, cudaStream_t st);
 cudaError_t launch_lat_fwd_tc(const Prob &p, const void *q, const void *c, void *o, float *lse, const LatWs &ws,
                               cudaStream_t st);
 cudaError_t launch_lat_fwd_simt(const Prob &p, const void *q, const void *c, const int32_t *anchors,

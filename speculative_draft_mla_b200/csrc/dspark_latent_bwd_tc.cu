@@ -657,40 +657,6 @@ bool make_acc_map(CUtensorMap *m, float *acc, uint64_t L, uint64_t B) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The queries' rope slices turned to their positions, hi then lo, and the
-// key gradients' accumulators cleared: 313 MB at S = 4096, N = 512, B = 4, about 50 us.
-__global__ void __launch_bounds__(256) k_lat_bwd_prep(const __nv_bfloat16 *__restrict__ q,
-                                                      const int32_t *__restrict__ anchors,
-                                                      const float2 *__restrict__ tab, __nv_bfloat16 *__restrict__ out,
-                                                      float4 *__restrict__ dacc, size_t rows, size_t acc4, int n_h, int N,
-                                                      int P) {
-    pdl_wait();
-    pdl_trigger();
-    const size_t t0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, nt = (size_t)gridDim.x * blockDim.x;
-    for (size_t e = t0; e < acc4; e += nt) dacc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int R = kBlock * N;
-    // eight threads to a row, four pairs each
-    for (size_t e = t0; e < rows * 8; e += nt) {
-        const size_t row = e >> 3;
-        const int u = (int)(e & 7), r = (int)(row % (unsigned)R), b = (int)(row / (unsigned)R / (unsigned)n_h);
-        const int pos = min(max(anchors[(size_t)b * N + r / kBlock] + r % kBlock, 0), P - 1);
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + row * kDK + kDL) + u);
-        const float4 *cs = reinterpret_cast<const float4 *>(tab + (size_t)pos * (kDR / 2)) + 2 * u;
-        const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
-        uint4 hi, lo;
-        auto turn = [](uint32_t w, float c, float s, uint32_t &h, uint32_t &l) {
-            const float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xffff0000u);
-            split_bf16x2(a * c - b * s, a * s + b * c, h, l);
-        };
-        turn(v.x, c0.x, c0.y, hi.x, lo.x);
-        turn(v.y, c0.z, c0.w, hi.y, lo.y);
-        turn(v.z, c1.x, c1.y, hi.z, lo.z);
-        turn(v.w, c1.z, c1.w, hi.w, lo.w);
-        reinterpret_cast<uint4 *>(out + row * 2 * kDR)[u] = hi;
-        reinterpret_cast<uint4 *>(out + row * 2 * kDR + kDR)[u] = lo;
-    }
-}
-
 // Accumulators to outputs: dc rounded, the rope part turned back to its
 // position and rounded. One warp per position.
 __global__ void __launch_bounds__(256) k_lat_bwd_out(const float *__restrict__ dacc, const int32_t *__restrict__ anchors,
@@ -723,19 +689,13 @@ bool lat_bwd_tc_supported(const Prob &p) { return lat_tc_supported(p); }
 
 cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const int32_t *anchors, const float *lse,
                               const void *dout, void *dq, void *dc, void *dkr, const LatWs &ws, cudaStream_t st) {
-    // (padding blocks' rows of dq are written by the preparation before this)
+    // (the preparation before this has written padding blocks' rows of dq, turned the
+    // queries' rope slices and cleared the accumulators)
     if (p.B == 0) return cudaSuccess;
     int dev = 0, nsm = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const size_t rows = (size_t)p.B * p.n_h * p.R, acc4 = (size_t)p.B * p.L * kDK / 4;
-    const size_t work = std::max(rows * 8, acc4);
-    count_launch();
-    e = launch_pdl(k_lat_bwd_prep, dim3((unsigned)std::min<size_t>((work + 255) / 256, (size_t)nsm * 8)), dim3(256), 0, st,
-                   (const __nv_bfloat16 *)q, anchors, (const float2 *)ws.base.rope, ws.q_rot, (float4 *)ws.dacc, rows,
-                   acc4, p.n_h, std::max(p.N, 1), p.P);
-    if (e != cudaSuccess) return e;
     if (p.N > 0) {
         Args a{};
         a.n_h = p.n_h; a.S = p.S; a.N = p.N; a.W = p.W; a.R = p.R; a.B = p.B; a.L = p.L;

@@ -178,7 +178,7 @@ dspark_status dspark_latent_attn_fwd(const dspark_latent_problem *pp, const void
     pad.rows[0] = p.R;
     pad.width[0] = p.d_c;
     pad.lse = lse;
-    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, tc ? &pad : nullptr, tc, w, st));
+    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, tc ? &pad : nullptr, tc, false, nullptr, w, st));
     if (tc)
         DSPARK_CUDA(launch_lat_fwd_tc(p, q, c, o, lse, w, st));
     else
@@ -206,7 +206,7 @@ dspark_status dspark_latent_attn_bwd(const dspark_latent_problem *pp, const void
     pad.t[0] = dq;
     pad.rows[0] = p.R;
     pad.width[0] = p.dqk;
-    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, tc ? &pad : nullptr, tc, w, st));
+    DSPARK_CUDA(launch_lat_prep(p, kr, anchors, keep, tc ? &pad : nullptr, tc, tc, q, w, st));
     if (tc)
         DSPARK_CUDA(launch_lat_bwd_tc(p, q, c, anchors, lse, do_, dq, dc, dkr, w, st));
     else

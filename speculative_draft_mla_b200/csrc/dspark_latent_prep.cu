@@ -3,7 +3,7 @@
 // attention kernels.
 #include <algorithm>
 
-#include "dspark_latent.cuh"
+#include "dspark_latent_tc.cuh"
 
 namespace dspark {
 
@@ -23,13 +23,46 @@ template <> struct Pair<__nv_bfloat16> { using V = __nv_bfloat162; };
 //   hi, lo: x = hi + lo to 2^-17, both bf16, for the tensor cores: with one
 //   bf16 the scores would be off by up to 2^-8 of their rope part, and the fp32
 //   LSE with them; with three products hi hi + lo hi + hi lo it keeps 2^-16.
-// CTA g also takes blocks g, g + G, ... and writes the padding ones' rows.
+// The warps also go over the blocks and write the padding ones' rows, and, before a
+// backward, turn the queries' rope slices and clear the accumulators.
+// The queries' rope slices turned to their positions, hi then lo, and the key
+// gradients' accumulators cleared: 313 MB at S = 4096, N = 512, B = 4, 48 us at the
+// measured copy rate, beside 76 MB of padding rows (in a launch of its own after the
+// padding rows: 14 us more).
+__device__ __forceinline__ void bwd_rows(const BwdPrep &w, const int32_t *__restrict__ anchors,
+                                         const float2 *__restrict__ tab, int n_h, int N, int P) {
+    const size_t t0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, nt = (size_t)gridDim.x * blockDim.x;
+    for (size_t e = t0; e < w.acc4; e += nt) w.acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int R = kBlock * N;
+    // eight threads to a row, four pairs each
+    for (size_t e = t0; e < w.rows * 8; e += nt) {
+        const size_t row = e >> 3;
+        const int u = (int)(e & 7), r = (int)(row % (unsigned)R), b = (int)(row / (unsigned)R / (unsigned)n_h);
+        const int pos = min(max(anchors[(size_t)b * N + r / kBlock] + r % kBlock, 0), P - 1);
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(w.q + row * (kTcDL + kTcDR) + kTcDL) + u);
+        const float4 *cs = reinterpret_cast<const float4 *>(tab + (size_t)pos * (kTcDR / 2)) + 2 * u;
+        const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
+        uint4 hi, lo;
+        auto turn = [](uint32_t x, float c, float s, uint32_t &h, uint32_t &l) {
+            const float a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xffff0000u);
+            tc::split_bf16x2(a * c - b * s, a * s + b * c, h, l);
+        };
+        turn(v.x, c0.x, c0.y, hi.x, lo.x);
+        turn(v.y, c0.z, c0.w, hi.y, lo.y);
+        turn(v.z, c1.x, c1.y, hi.z, lo.z);
+        turn(v.w, c1.z, c1.w, hi.w, lo.w);
+        reinterpret_cast<uint4 *>(w.out + row * 2 * kTcDR)[u] = hi;
+        reinterpret_cast<uint4 *>(w.out + row * 2 * kTcDR + kTcDR)[u] = lo;
+    }
+}
+
+constexpr int kPadHeads = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) k_lat_prep(const T *__restrict__ kr, const int32_t *__restrict__ anchors,
                                                   const uint8_t *__restrict__ keep, const float2 *__restrict__ tab,
                                                   float *__restrict__ f32, __nv_bfloat16 *__restrict__ hi,
                                                   __nv_bfloat16 *__restrict__ lo, int B, int S, int N, int L, int d_r,
-                                                  int P, int n_h, int pad_blocks, PadRows pad) {
+                                                  int P, int n_h, int pad_blocks, PadRows pad, BwdPrep bw) {
     pdl_wait();
     pdl_trigger();
     const int half = d_r / 2, lane = threadIdx.x & 31;
@@ -72,36 +105,46 @@ __global__ void __launch_bounds__(256) k_lat_prep(const T *__restrict__ kr, cons
             }
         }
     }
+    // padding blocks: one warp to a block's eight heads
     const uint4 z = make_uint4(0, 0, 0, 0);
-    for (int id = blockIdx.x; id < pad_blocks; id += gridDim.x) {
-        const int n = id % N, b = id / N;
+    const int groups = (n_h + kPadHeads - 1) / kPadHeads;
+    const long long units = (long long)pad_blocks * groups, step = (long long)gridDim.x * 8;
+    for (long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); id < units; id += step) {
+        const int g = (int)(id % groups), n = (int)(id / groups % N), b = (int)(id / groups / N);
         const int a = anchors[(size_t)b * N + n];
         if (keep[(size_t)b * N + n] && a >= 0 && a <= S - 2) continue;
-#pragma unroll
-        for (int k = 0; k < 3; k++) {
-            if (!pad.t[k]) continue;
-            // t[0] belongs to the heads, t[1] and t[2] are shared by them
-            const int w8 = pad.width[k] / 8, heads = k == 0 ? n_h : 1;
-            for (int h = 0; h < heads; h++) {
-                uint4 *dst = reinterpret_cast<uint4 *>(
-                    reinterpret_cast<__nv_bfloat16 *>(pad.t[k]) +
-                    (((size_t)b * heads + h) * pad.rows[k] + pad.first[k] + (size_t)kBlock * n) * pad.width[k]);
-                for (int e = threadIdx.x; e < kBlock * w8; e += blockDim.x) dst[e] = z;
-            }
+        const int h0 = g * kPadHeads, h1 = min(n_h, h0 + kPadHeads), w8 = pad.width[0] / 8;
+        for (int h = h0; h < h1; h++) {
+            uint4 *dst = reinterpret_cast<uint4 *>(
+                reinterpret_cast<__nv_bfloat16 *>(pad.t[0]) +
+                (((size_t)b * n_h + h) * pad.rows[0] + (size_t)kBlock * n) * pad.width[0]);
+            for (int e = lane; e < kBlock * w8; e += 32) dst[e] = z;
         }
         if (pad.lse)
-            for (int e = threadIdx.x; e < kBlock * n_h; e += blockDim.x)
+            for (int e = kBlock * h0 + lane; e < kBlock * h1; e += 32)
                 pad.lse[((size_t)b * n_h + e / kBlock) * kBlock * N + (size_t)kBlock * n + e % kBlock] = -INFINITY;
     }
+    if constexpr (sizeof(T) == 2)
+        if (bw.acc) bwd_rows(bw, anchors, tab, n_h, N, P);
 }
 
 }  // namespace
 
 cudaError_t launch_lat_prep(const Prob &p, const void *kr, const int32_t *anchors, const uint8_t *keep,
-                            const PadRows *pad, bool tc, const LatWs &ws, cudaStream_t st) {
+                            const PadRows *pad, bool tc, bool bwd, const void *q, const LatWs &ws, cudaStream_t st) {
     const size_t rows = p.d_r > 0 ? (size_t)p.B * p.L : 0;
     const int pad_blocks = pad ? p.N * p.B : 0;
-    const unsigned grid = (unsigned)std::max<size_t>((rows + 31) / 32, (size_t)std::min(pad_blocks, 148 * 4));
+    const size_t units = (size_t)pad_blocks * ((p.n_h + kPadHeads - 1) / kPadHeads);
+    BwdPrep bw{};
+    if (bwd) {
+        bw.q = (const __nv_bfloat16 *)q;
+        bw.out = ws.q_rot;
+        bw.acc = (float4 *)ws.dacc;
+        bw.rows = (size_t)p.B * p.n_h * p.R;
+        bw.acc4 = (size_t)p.B * p.L * (kTcDL + kTcDR) / 4;
+    }
+    const size_t most = std::max({(units + 7) / 8, (bw.acc4 + 255) / 256, (bw.rows * 8 + 255) / 256});
+    const unsigned grid = (unsigned)std::max<size_t>((rows + 31) / 32, std::min<size_t>(most, 148 * 8));
     if (grid == 0) return cudaSuccess;
     PadRows pr{};
     if (pad) pr = *pad;
@@ -111,10 +154,10 @@ cudaError_t launch_lat_prep(const Prob &p, const void *kr, const int32_t *anchor
     if (p.dtype == DSPARK_BF16)
         return launch_pdl(k_lat_prep<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, (const __nv_bfloat16 *)kr, anchors,
                           keep, (const float2 *)ws.base.rope, f32, hi, lo, p.B, p.S, p.N, p.L, p.d_r, p.P, p.n_h,
-                          pad_blocks, pr);
+                          pad_blocks, pr, bw);
     return launch_pdl(k_lat_prep<float>, dim3(grid), dim3(256), 0, st, (const float *)kr, anchors, keep,
                       (const float2 *)ws.base.rope, f32, hi, lo, p.B, p.S, p.N, p.L, p.d_r, p.P, p.n_h, pad_blocks,
-                      pr);
+                      pr, bw);
 }
 
 }  // namespace dspark

@@ -89,7 +89,8 @@ __device__ __forceinline__ void red4(float *a, float x, float y, float z, float 
 }
 // A box of shared memory added to fp32 rows.
 __device__ __forceinline__ void tma_red_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)m),
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     (uint64_t)m),
                  "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
@@ -134,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_c,
                  const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_l,
                  const __grid_constant__ CUtensorMap tm_c5, const __grid_constant__ CUtensorMap tm_h5,
-                 const __grid_constant__ CUtensorMap tm_l5, const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_acc, const Args p) {
+                 const __grid_constant__ CUtensorMap tm_l5, const __grid_constant__ CUtensorMap tm_dq,
+                 const __grid_constant__ CUtensorMap tm_acc, const Args p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     // a slot's full barriers: [0] of copies for the gradients, [1] of those for the scores
@@ -142,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *qfull = kempty + kKSlots, *qempty = qfull + 2 * kPairs2;
     uint64_t *sfull = qempty + kPairs2, *pds = sfull + 1, *drain = sfull + 2;
     uint64_t *qcfull = sfull + 5, *qcfree = qcfull + 1, *kcfull = qcfull + 2, *kcfree = kcfull + 2;
-    uint64_t *dfull = kcfree + 2, *dfree = dfull + 1, *done = dfull + 2, *lbar = done + 2, *ofull = lbar + 4, *ofree = ofull + 1;
+    uint64_t *dfull = kcfree + 2, *dfree = dfull + 1, *done = dfull + 2, *lbar = done + 2;
+    uint64_t *ofull = lbar + 4, *ofree = ofull + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ofree + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ofree + 2);
     float *xd = reinterpret_cast<float *>(sm + oX);
@@ -727,7 +730,8 @@ cudaError_t launch_lat_bwd_tc(const Prob &p, const void *q, const void *c, const
         const uint64_t cd[3] = {kDL, L, B}, cs[2] = {kDL * 2, L * kDL * 2};
         const uint64_t rd[3] = {kDR, L, B}, rs[2] = {kDR * 2, L * kDR * 2};
         const uint32_t wb[3] = {64, (uint32_t)std::max(p.W - 1, 1), 1}, db[3] = {64, kBlock, 1};
-        if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mdq, dq, 4, qd, qs, qb) || !make_map_nd(&mg, dout, 4, gd, gs, qb) ||
+        if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mdq, dq, 4, qd, qs, qb) ||
+            !make_map_nd(&mg, dout, 4, gd, gs, qb) ||
             !make_map_nd(&mr, ws.q_rot, 4, sd, ss, qb) || !make_map_nd(&mc, c, 3, cd, cs, wb) ||
             !make_map_nd(&mh, ws.kr_hi, 3, rd, rs, wb) || !make_map_nd(&mc5, c, 3, cd, cs, db) ||
             !make_map_nd(&mh5, ws.kr_hi, 3, rd, rs, db) || !make_map_nd(&ml, ws.kr_lo, 3, rd, rs, wb) ||

@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 mma_commit_warp(&kempty[2 * st]);
                 if (!wait(&kfull[2 * st + 1], (g >> 1) & 1)) break;
                 tc_fence_after();
-                four(uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 16, kGroupB))), half != 0, false);
+                four(uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 16, kGroupB))), half != 0,
+                     false);
                 if (t + 1 == sg.s1) mma_commit_warp(qfree);
                 mma_commit_warp(sfull);
             }
@@ -498,7 +499,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 const SDesc vd = uniform(sdesc_split(sdesc_sw128(smem_u32(sm) + st * kStage + oPartB, 1024, kGroupB)));
 #pragma unroll
                 for (int u = 0; u < 4; u++)
-                    mma_bf16_ss_warp(tm + kColO, pd.at(2 * u), vd.at(2 * (kGroupB / 16) * u), idO, t != sg.s0 || u > 0 ? 1u : 0u);
+                    mma_bf16_ss_warp(tm + kColO, pd.at(2 * u), vd.at(2 * (kGroupB / 16) * u), idO,
+                                     t != sg.s0 || u > 0 ? 1u : 0u);
                 mma_commit_warp(&kempty[2 * st + 1]);
                 mma_commit_warp(pvdone);
             }
@@ -817,7 +819,8 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
 }
 
 template <int KIND>
-cudaError_t launch_t(const CUtensorMap &m4, const CUtensorMap &m1, const CUtensorMap &mq, const Paged &p, const PagedPlan &w, cudaStream_t st) {
+cudaError_t launch_t(const CUtensorMap &m4, const CUtensorMap &m1, const CUtensorMap &mq, const Paged &p,
+                     const PagedPlan &w, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(k_paged_tc<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     count_launch();

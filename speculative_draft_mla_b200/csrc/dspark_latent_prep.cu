@@ -1,6 +1,6 @@
-// Rope keys of the latent draft attention turned to their positions, and the
-// rows of padding blocks: the launch between the mask descriptor and the
-// attention kernels.
+// Rope keys of the latent draft attention turned to their positions, the rows of
+// padding blocks, and what else a backward starts from: the launch between the mask
+// descriptor and the attention kernels.
 #include <algorithm>
 
 #include "dspark_latent_tc.cuh"

@@ -62,7 +62,7 @@ def test_draft_waits_run_out_and_the_context_recovers():
 
 @pytest.mark.parametrize("name,kind", [("long", "bf16"), ("short", "bf16"), ("short", "fp8")])
 def test_paged_waits_run_out_and_the_context_recovers(name, kind):
-    n_seq, q_len, kv_len, window = (2, 20, 40000, 0) if name == "long" else (300, 5, 200, 128)
+    n_seq, q_len, kv_len, window = (2, 20, 120000, 0) if name == "long" else (300, 5, 200, 128)
     cache, _, _ = filled(72, kind, 64, 16, 512, 64)
     g = torch.Generator().manual_seed(73)
     table = torch.randint(0, 64, (n_seq, -(-kv_len // 16)), generator=g, dtype=torch.int32)

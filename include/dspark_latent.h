@@ -141,9 +141,12 @@ DSPARK_API dspark_status dspark_latent_cache_read(const dspark_latent_cache *p, 
  *     and below 2^39; both 0 = contiguous); lse [T, n_h] fp32 contiguous
  *   q_start [n_seq + 1], kv_len [n_seq], block_table [n_seq, max_pages]: int32
  * A page outside [0, n_pages), a kv_len outside [0, max_pages * page_size] or a
- * q_start that is not ascending within [0, T] is only visible on the device: the
- * page's keys are skipped, the sequence gives O = 0 and LSE = -inf (or, for
- * q_start, nothing), and dspark_get_error returns DSPARK_ERR_PAGE.
+ * q_start that is not ascending within [0, T] is only visible on the device, and
+ * dspark_get_error returns DSPARK_ERR_PAGE: the page's keys are skipped; a sequence
+ * of such a kv_len gives O = 0 and LSE = -inf; one whose two q_start entries descend
+ * or leave [0, T], or that begins before the end of an earlier sequence whose
+ * entries do not, attends nothing and leaves rows as they were. The other
+ * sequences are not affected.
  * kind F32 goes with dtype F32, BF16 and FP8 with dtype BF16.
  * Limits: n_h >= 1, n_seq >= 0, T >= 0, page_size >= 1, widths as the cache,
  *   T * n_h < 2^31, max_pages * page_size < 2^31, n_pages * page_size < 2^31,

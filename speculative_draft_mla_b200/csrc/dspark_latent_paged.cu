@@ -10,11 +10,17 @@ namespace {
 
 // One launch ahead of the attention. CTA 0 writes the error word (the page bit
 // for a q_start or kv_len out of range, else 0; pages are checked by the
-// kernels that read them) and, for the tensor-core kernel, the list of row
-// tiles: tile r is up to 128 (token, head) rows of one sequence and takes
-// its steps of 64 keys, at least one. The CTA pairs of the
+// kernels that read them) and, for the tensor-core kernels, the list of short
+// sequences and the list of row tiles: tile r is up to 128 (token, head) rows of
+// one sequence and takes its steps of 64 keys, at least one. The CTA pairs of the
 // attention share all steps evenly, wherever tiles begin and end; first[i] is
 // the tile that pair i begins in. The other CTAs fill the tokens' (cos, sin).
+//
+// A sequence that begins before the end of an earlier one (of any whose own two
+// entries are in order, refused or not) attends nothing. So those that attend
+// share no token: no row has two writers, the first sequence that holds a token
+// is its only one (what the search below and the CUDA-core kernel rely on), and
+// their tiles, fewer than 2^26 as T * n_h < 2^31, fit the list.
 __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedPlan w, int tc, int shorts, int tab_ctas) {
     pdl_wait();
     pdl_trigger();
@@ -39,13 +45,14 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         return;
     }
     __shared__ long long wsteps[32], carry_steps;
-    __shared__ int wtiles[32], carry_tiles, bad, n_split, n_short;
+    __shared__ int wtiles[32], wends[32], carry_tiles, carry_end, bad, n_split, n_short;
     if (threadIdx.x == 0) {
         bad = 0;
         n_split = 0;
         n_short = 0;
         carry_steps = 0;
         carry_tiles = 0;
+        carry_end = 0;
     }
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -54,8 +61,25 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         SeqView v{};
         int nt = 0;
         long long ns = 0;
+        if (s < p.n_seq) v = seq_view(p, s);
+        // the last end of the sequences before this one
+        const int end = v.q_len > 0 ? v.q0 + v.q_len : 0;
+        int upto = end;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto = max(upto, a);
+        }
+        if (lane == 31) wends[warp] = upto;
+        int before = __shfl_up_sync(0xffffffffu, upto, 1);
+        __syncthreads();
+        before = lane > 0 ? max(before, carry_end) : carry_end;
+        for (int k = 0; k < warp; k++) before = max(before, wends[k]);
         if (s < p.n_seq) {
-            v = seq_view(p, s);
+            if (v.q_len > 0 && v.q0 < before) {
+                v.q_len = 0;
+                v.bad = true;
+            }
             if (v.bad) bad = 1;
             bool brief = false;
             if (shorts && v.q_len > 0) {
@@ -72,7 +96,6 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
                 ns *= w.hchunks;
             }
         }
-        if (!tc) continue;
         // inclusive sums over the block
         int it = nt;
         long long is = ns;
@@ -100,14 +123,10 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         if (threadIdx.x == blockDim.x - 1) {
             carry_tiles = bt + nt;
             carry_steps = bs + ns;
+            carry_end = max(before, end);
         }
         for (int t = 0; t < nt; t++) {
             const int hc = t % w.hchunks, i0 = t / w.hchunks * w.tpt;
-            // (sequences that overlap, an error, could need more tiles than there is room for)
-            if (bt + t >= w.max_tiles) {
-                bad = 1;
-                break;
-            }
             PagedTile o;
             o.seq = s;
             o.i0 = i0;
@@ -125,9 +144,8 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
     }
     __syncthreads();
     if (tc) {
-        const int n = min(carry_tiles, w.max_tiles);
-        long long total = carry_steps;
-        if (carry_tiles > w.max_tiles) total = 0;  // overlapping sequences: nothing is attended
+        const int n = carry_tiles;
+        const long long total = carry_steps;
         const long long X = (total + kPairs - 1) / kPairs;
         if (threadIdx.x == 0) {
             w.head->total = total;

@@ -294,19 +294,24 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_simt(const Paged p) {
     const long long id = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (id >= (long long)p.T * p.n_h) return;
     const int tok = (int)(id / p.n_h), h = (int)(id % p.n_h);
-    // the sequence of the token: the warp scans the starts 32 at a time
-    int s = -1;
+    // the sequence of the token: the warp scans the starts 32 at a time, and keeps the
+    // last end before it (a sequence that begins before that attends nothing)
+    int s = -1, before = 0;
     for (int s0 = 0; s0 < p.n_seq && s < 0; s0 += 32) {
         bool mine = false;
+        int end = 0;
         if (s0 + lane < p.n_seq) {
             const SeqView v = seq_view(p, s0 + lane);
             mine = tok >= v.q0 && tok < v.q0 + v.q_len;
+            if (v.q_len > 0) end = v.q0 + v.q_len;
         }
         const unsigned any = __ballot_sync(0xffffffffu, mine);
         if (any) s = s0 + __ffs(any) - 1;
+        if (s < 0 || s0 + lane < s) before = max(before, end);
     }
     if (s < 0) return;  // behind the last sequence
     const SeqView sv = seq_view(p, s);
+    if (__any_sync(0xffffffffu, sv.q0 < before)) return;
     int lo, hi;
     seq_range(p, sv, tok - sv.q0, &lo, &hi);
     const T *qrow = (const T *)p.q + (long long)tok * p.q_ts + (long long)h * p.q_hs;

@@ -56,30 +56,39 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
     }
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int disorder = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += blockDim.x) {
         const int s = s0 + threadIdx.x;
         SeqView v{};
         int nt = 0;
         long long ns = 0;
         if (s < p.n_seq) v = seq_view(p, s);
-        // the last end of the sequences before this one
-        const int end = v.q_len > 0 ? v.q0 + v.q_len : 0;
-        int upto = end;
+        // (in order so far: none begins before an earlier one's end)
+        disorder |= __syncthreads_or(v.bad);
+        if (disorder) {
+            const int end = v.q_len > 0 ? v.q0 + v.q_len : 0;
+            int upto = end;  // the last end of the sequences up to this one
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto = max(upto, a);
-        }
-        if (lane == 31) wends[warp] = upto;
-        int before = __shfl_up_sync(0xffffffffu, upto, 1);
-        __syncthreads();
-        before = lane > 0 ? max(before, carry_end) : carry_end;
-        for (int k = 0; k < warp; k++) before = max(before, wends[k]);
-        if (s < p.n_seq) {
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto = max(upto, a);
+            }
+            if (lane == 31) wends[warp] = upto;
+            const int last = __shfl_up_sync(0xffffffffu, upto, 1);
+            __syncthreads();
+            int before = max(carry_end, lane > 0 ? last : 0);
+            for (int k = 0; k < warp; k++) before = max(before, wends[k]);
+            __syncthreads();
+            if (threadIdx.x == blockDim.x - 1) carry_end = max(before, end);
             if (v.q_len > 0 && v.q0 < before) {
                 v.q_len = 0;
                 v.bad = true;
             }
+        } else if (threadIdx.x == 0 && s0 + (int)blockDim.x < p.n_seq) {
+            const int next = p.q_start[s0 + blockDim.x];
+            carry_end = next > p.q_start[0] ? next : 0;
+        }
+        if (s < p.n_seq) {
             if (v.bad) bad = 1;
             bool brief = false;
             if (shorts && v.q_len > 0) {
@@ -123,7 +132,6 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         if (threadIdx.x == blockDim.x - 1) {
             carry_tiles = bt + nt;
             carry_steps = bs + ns;
-            carry_end = max(before, end);
         }
         for (int t = 0; t < nt; t++) {
             const int hc = t % w.hchunks, i0 = t / w.hchunks * w.tpt;

@@ -65,6 +65,37 @@ def test_wrong_starts_leave_the_others(name, kind, kv_len, window):
     assert bool((o[left] == 5).all()) and bool((lse[left] == 9).all())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["behind a thousand", "empty ones first"])
+def test_wrong_starts_far_down_the_list(name, kind):
+    """More sequences than the plan's threads: what came before is carried on."""
+    if name == "behind a thousand":
+        starts, good = list(range(1031)) + [500, 503, 1030, 1033], list(range(1030)) + [1033]
+    else:
+        starts, good = [5] * 1030 + [0, 3, 3, 4, 5], [1030, 1032, 1033]
+    n, T, n_h = len(starts) - 1, max(starts), 3
+    cache, lat, rope = filled(15, kind, 12, PAGE, 512, 64)
+    g = torch.Generator().manual_seed(16)
+    table = torch.randint(0, 12, (n, 10), generator=g, dtype=torch.int32)
+    q = torch.randn(T, n_h, 576, generator=g).to(torch.float32 if kind == "f32" else torch.bfloat16)
+    kv = torch.randint(1, 30, (n,), generator=g, dtype=torch.int32)
+    out = torch.full((T, n_h, 512), 5.0, dtype=q.dtype, device="cuda"), torch.full((T, n_h), 9.0, device="cuda")
+    o, lse, ws = capi.latent_attn_paged(q.cuda(), cache, table.cuda(), torch.tensor(starts, dtype=torch.int32).cuda(),
+                                        kv.cuda(), out=out)
+    reported(ws)
+    left = torch.ones(T, dtype=torch.bool)
+    for s in good:
+        a, b = starts[s], starts[s + 1]
+        left[a:b] = False
+        if a % 97 and s + 4 < n:
+            continue
+        val, err = reference(q[a:b].double().numpy(), lat, rope, table[s:s + 1].numpy(), [0, b - a], kv[s:s + 1].numpy(),
+                             PAGE, capi.LATENT_SCALE, True, 0, kind != "f32")
+        lp.check("o", o[a:b], val["o"], err["o"])
+        lp.check("lse", lse[a:b], val["lse"], err["lse"])
+    assert bool((o[left] == 5).all()) and bool((lse[left] == 9).all()) and not bool((lse[~left] == 9).any())
+
+
 def test_ranges_repeated_until_their_tiles_pass_32_bits():
     """2^17 sequences over the same 128 tokens of 16385 heads: 2.2e9 row tiles if all of them attended. The first does."""
     T, n_h, n, kv_len = 128, 16385, 1 << 18, 150

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
         }
         for (int t = 0; t < nt; t++) {
             const int hc = t % w.hchunks, i0 = t / w.hchunks * w.tpt;
-            PagedTile o;
+            PagedTile o{};
             o.seq = s;
             o.i0 = i0;
             o.hc = hc;
@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(1024) k_paged_plan(const Paged p, const PagedP
             w.head->total = total;
             w.head->per = X;
             w.head->n_short = n_short;
+            w.head->n_tiles = n;
+            w.head->redo = 0;
         }
         __syncthreads();
         if (total)

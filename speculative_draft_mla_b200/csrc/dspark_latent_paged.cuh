@@ -14,11 +14,14 @@ struct PagedHead {
     long long total, per;  // steps of all tiles; steps of a pair
     int n_split;           // tiles that several pairs work on
     int n_short;           // sequences of the short kernel
+    int n_tiles;
+    int redo;              // whether a tile has rows to evaluate again
 };
 struct alignas(16) PagedTile {      // up to 128 (token, head) rows of a sequence
     int seq, i0, hc, q_len;  // first token within the sequence, chunk of 128 heads
     int q0, kv, lo, hi;      // the sequence's first token; keys; keys that some row sees
     long long start, steps;  // its steps in the list of all
+    uint32_t redo[4];        // rows to evaluate again
 };
 struct PagedPlan {
     PagedHead *head;

@@ -18,7 +18,9 @@
 // else row by row (TMA gathers of 4 rows x 64 columns, which need no groups, took
 // 64 cycles each and were twice as slow); 8-bit rows through registers, where they
 // become bf16 (exact: a scale is a power of two). Slots of keys that no row of the
-// tile sees are zero, and a row's weight of a key outside its own range is zero.
+// tile sees are zero, and a row's weight of a key outside its own range is zero. A
+// row that sees NaN or +inf is NaN; one whose tile holds a key that is not finite
+// and that it does not see has met 0 x NaN, and the last launch evaluates it again.
 //
 // A CTA holds two steps of keys; the five slices that only S needs (the other
 // half's values, the rope keys) are free for the step after next once S is formed,
@@ -536,12 +538,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 rm &= km;
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 if (!warp_all(rm == 0xffffffffu)) {
+                    float far = 0.f;  // 0, or NaN (0 x NaN, 0 x infinity)
 #pragma unroll
                     for (int c = 0; c < 32; c++) {
                         const bool in = (rm >> c) & 1;
-                        bad |= !in && !(fabsf(s[c]) < INFINITY);
+                        far = in ? far : fmaf(0.f, s[c], far);
                         s[c] = in ? s[c] : -INFINITY;
                     }
+                    bad |= far != 0.f;
                 }
 #pragma unroll
                 for (int c = 0; c < 32; c++) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
@@ -604,21 +608,29 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 if (lane == 0) mbar_arrive(pready);
             }
             if (!ok) break;
-            xm[((g & 1) * 2 + hf) * 128 + r] = bad ? NAN : l;
+            // A row's share of the sums: NaN where a key of its own is not finite; else
+            // -1 where one that it does not see is not: its product with that key was not
+            // zero (0 x NaN), and it is left to the last launch.
+            const float mine = bad && l == l ? -1.f : l;
+            xm[((g & 1) * 2 + hf) * 128 + r] = mine;
             __syncwarp();
             if (lane == 0) mbar_arrive(&lbar[q4]);
             ok = warp_all(mbar_wait(pvdone, (g - 1) & 1, abort_flag, wlim)) &&
                  warp_all(mbar_wait(&lbar[q4], 0, abort_flag, wlim));
             if (!ok) break;
             tc_fence_after();
-            // (a row that sees NaN or infinity itself has NaN sums too, and comes
-            // out the same either way)
-            const float lt = (bad ? NAN : l) + xm[((g & 1) * 2 + (hf ^ 1)) * 128 + r];
+            const float theirs = xm[((g & 1) * 2 + (hf ^ 1)) * 128 + r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&lbar[q4]);
-            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const float lt = mine + theirs;
+            const uint32_t redo = __ballot_sync(0xffffffffu, live && lt == lt && (mine < 0.f || theirs < 0.f));
+            if (redo && lane == 0) {
+                atomicOr(&w.tiles[cur.r - 1].redo[q4], redo);
+                w.head->redo = 1;
+            }
             const int tok = sg.tok0 + ti, col0 = 256 * half + 128 * hf;
-            const float lse2 = lt > 0.f ? m + log2f(lt) : -INFINITY;
+            const float none = lt != lt ? lt : 0.f;  // of a row that sees no key, or NaN
+            const float lse2 = lt > 0.f ? m + log2f(lt) : lt != lt ? lt : -INFINITY;
             uint8_t *dst = nullptr;
             float *pdst = nullptr;
             if (sg.slot >= 0) {
@@ -628,7 +640,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 dst = (uint8_t *)((__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs + col0);
                 if (half == 0 && hf == 0) p.lse[(size_t)tok * p.n_h + h] = lse2 * kLn2;
             }
-            const float f = lt > 0.f ? inv : 0.f;
+            const float f = lt > 0.f ? 1.f / lt : 0.f;
             const bool wide = ((uintptr_t)dst & 31) == 0;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
@@ -637,7 +649,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 tmem_wait_ld();
                 // (a row that sees no key may hold what was there before)
 #pragma unroll
-                for (int i = 0; i < 32; i++) o[i] = lt > 0.f ? o[i] * f : 0.f;
+                for (int i = 0; i < 32; i++) o[i] = lt > 0.f ? o[i] * f : none;
                 if (pdst && live) {
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
@@ -659,39 +671,6 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(ofree);
-            // Rows whose product met a key that is not finite and not theirs (0 x NaN):
-            // the whole warp evaluates them one by one over the row's own keys.
-            __syncwarp();
-            uint32_t redo = __ballot_sync(0xffffffffu, live && lt != lt);
-            while (redo) {
-                const int who = __ffs(redo) - 1;
-                redo &= redo - 1;
-                const int rti = __shfl_sync(0xffffffffu, ti, who), rh = __shfl_sync(0xffffffffu, h, who);
-                const int ka = max(__shfl_sync(0xffffffffu, lo, who), sg.base + sg.s0 * kStepKeys);
-                const int kb = min(__shfl_sync(0xffffffffu, hi, who), sg.base + sg.s1 * kStepKeys);
-                const int rtok = sg.tok0 + rti;
-                float acc[18], rmx, rl;
-                paged_row<__nv_bfloat16, KIND, 18, 1>(
-                    p, sg.seq, (const __nv_bfloat16 *)p.q + (long long)rtok * p.q_ts + (long long)rh * p.q_hs,
-                    sg.kv - sg.q_len + sg.i0 + rti, ka, kb, acc, rmx, rl);
-                const bool rsome = rl != 0.f;
-                const float ri = rsome ? 1.f / rl : 0.f, rlse = rsome ? rmx + log2f(rl) : -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int d = lane + 32 * i;
-                    if (d < col0 || d >= col0 + 128) continue;
-                    const float val = rsome ? acc[i] * ri : 0.f;
-                    if (sg.slot >= 0)
-                        w.part_o[((size_t)sg.slot * 128 + q4 * 32 + who) * kDL + d] = val;
-                    else
-                        ((__nv_bfloat16 *)p.o)[(long long)rtok * p.o_ts + (long long)rh * p.o_hs + d] =
-                            __float2bfloat16_rn(val);
-                }
-                if (lane == 0 && half == 0 && hf == 0) {
-                    if (sg.slot >= 0) w.part_lse[sg.slot * 128 + q4 * 32 + who] = rlse;
-                    else p.lse[(size_t)rtok * p.n_h + rh] = rlse * kLn2;
-                }
-            }
         }
     }
 
@@ -715,7 +694,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
 }
 
-// Joins the parts of the tiles that pairs shared: part k of a tile is pair
+// The last launch joins the parts of the tiles that pairs shared, and evaluates
+// rows again that met a foreign value that is not finite. Part k of a tile is pair
 // p0 + k's, in its slot 1 for the tile's beginning, 0 after it.
 __device__ __forceinline__ size_t part_row(int p0, int k, int row) {
     return (size_t)(2 * (p0 + k) + (k == 0)) * 128 + row;
@@ -724,12 +704,119 @@ __device__ __forceinline__ size_t part_row(int p0, int k, int row) {
 // row to a CTA: four groups of 128 threads take every fourth part, four columns
 // to a thread.
 constexpr int kFew = 8;
-__global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPlan w) {
+constexpr int kJoinSmem = 3 * 128 * 16;
+
+// Evaluates rows again whose product met a key that is not finite and that they do
+// not see: over their own keys, a row to a CTA, its keys in 16 runs, one to a warp.
+// Here, after the attention, no wait of that kernel stands on it (in its softmax
+// warps a NaN beside 6 tokens over 16384 keys took 80 - 280 ms, and time-outs were
+// near), and all SMs share the rows.
+template <int KIND> __device__ __forceinline__ void redo_rows(const Paged &p, const PagedPlan &w, uint8_t *smem) {
+    constexpr int kAtOnce = 64;  // tiles whose masks are looked at together
+    uint4 *masks = reinterpret_cast<uint4 *>(smem);
+    float *qs = reinterpret_cast<float *>(masks + kAtOnce), *col = qs + kDL + kDR, *pm = col + kDL, *pl = pm + 16;
+    static_assert(kAtOnce * 16 + (2 * kDL + kDR + 32) * 4 <= kJoinSmem, "shared memory");
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = w.head->n_tiles;
+    uint32_t seen = 0;  // rows so far: they are dealt to the CTAs in turn
+    for (int t0 = 0; t0 < n; t0 += kAtOnce) {
+        uint4 mine = make_uint4(0, 0, 0, 0);
+        if (threadIdx.x < kAtOnce && t0 + (int)threadIdx.x < n) {
+            mine = *reinterpret_cast<const uint4 *>(w.tiles[t0 + threadIdx.x].redo);
+            masks[threadIdx.x] = mine;
+        }
+        const bool some_tile = __syncthreads_or((mine.x | mine.y | mine.z | mine.w) != 0);
+        for (int t = t0; some_tile && t < min(n, t0 + kAtOnce); t++)
+            for (int q4 = 0; q4 < 4; q4++)
+                for (uint32_t rows = reinterpret_cast<const uint32_t *>(&masks[t - t0])[q4]; rows; rows &= rows - 1) {
+                    if (seen++ % gridDim.x != blockIdx.x) continue;
+                    const PagedTile &tl = w.tiles[t];
+                    const int row = 32 * q4 + __ffs(rows) - 1;
+                    const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.hc * 128 + row - ti * p.n_h;
+                    const int i = tl.i0 + ti, tok = tl.q0 + i;
+                    const SeqView v{tl.q0, tl.q_len, tl.kv, false};
+                    int lo, hi;
+                    seq_range(p, v, i, &lo, &hi);
+                    // the query, its rope slice turned, for all warps
+                    const __nv_bfloat16 *qrow =
+                        (const __nv_bfloat16 *)p.q + (long long)tok * p.q_ts + (long long)h * p.q_hs;
+                    __syncthreads();  // the row before is done
+                    qs[threadIdx.x] = to_f(qrow[threadIdx.x]);
+                    if (threadIdx.x < kDR / 2) {
+                        const float2 t = w.tab[(size_t)tok * 32 + threadIdx.x];
+                        const float x0 = to_f(qrow[kDL + 2 * threadIdx.x]), x1 = to_f(qrow[kDL + 2 * threadIdx.x + 1]);
+                        qs[kDL + 2 * threadIdx.x] = x0 * t.x - x1 * t.y;
+                        qs[kDL + 2 * threadIdx.x + 1] = x0 * t.y + x1 * t.x;
+                    }
+                    __syncthreads();
+                    // the warp's run of keys: acc = sum 2^(s - m) c, l the sum of the weights
+                    float acc[kDL / 32], m = -INFINITY, l = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kDL / 32; e++) acc[e] = 0.f;
+                    const int run = (hi - lo + 15) / 16, k0 = min(hi, lo + warp * run), k1 = min(hi, k0 + run);
+                    for (int key = k0; key < k1; key++) {
+                        const long long slot = key_slot(p, tl.seq, key);
+                        if (slot < 0) continue;  // (a page out of range, reported by the attention)
+                        const uint8_t *krow = (const uint8_t *)p.cache + (size_t)slot * p.row_bytes;
+                        float c[kDL / 32], x[1] = {0.f};
+#pragma unroll
+                        for (int e = 0; e < kDR / 32; e++)
+                            x[0] = fmaf(qs[kDL + lane + 32 * e], CacheRow<KIND>::at(krow, kDL + lane + 32 * e, kDL, kDR), x[0]);
+#pragma unroll
+                        for (int e = 0; e < kDL / 32; e++) {
+                            c[e] = CacheRow<KIND>::at(krow, lane + 32 * e, kDL, kDR);
+                            x[0] = fmaf(qs[lane + 32 * e], c[e], x[0]);
+                        }
+                        warp_sum_all(x);
+                        const float sc = x[0] * p.scale_log2, mn = fmaxf(m, sc);
+                        const float mu = mn == -INFINITY ? 0.f : mn;  // (scores of -inf or NaN only)
+                        const float old = exp2f(m - mu), f = exp2f(sc - mu);
+                        l = fmaf(l, old, f);
+#pragma unroll
+                        for (int e = 0; e < kDL / 32; e++) acc[e] = fmaf(acc[e], old, f * c[e]);
+                        m = mn;
+                    }
+                    if (lane == 0) {
+                        pm[warp] = m;
+                        pl[warp] = l;
+                    }
+                    col[threadIdx.x] = 0.f;
+                    __syncthreads();
+                    float mx = -INFINITY, sum = 0.f;
+                    for (int k = 0; k < 16; k++) mx = fmaxf(mx, pm[k]);
+                    // (a run of no key, or of scores of -inf or NaN: its l is 0 or NaN)
+                    const auto weight = [&](float x) { return x == -INFINITY ? 1.f : exp2f(x - mx); };
+                    for (int k = 0; k < 16; k++) {
+                        sum = fmaf(weight(pm[k]), pl[k], sum);
+                        if (warp == k) {
+                            const float f = weight(m);
+#pragma unroll
+                            for (int e = 0; e < kDL / 32; e++) col[lane + 32 * e] = fmaf(f, acc[e], col[lane + 32 * e]);
+                        }
+                        __syncthreads();
+                    }
+                    const bool some = sum != 0.f;
+                    ((__nv_bfloat16 *)p.o)[(long long)tok * p.o_ts + (long long)h * p.o_hs + threadIdx.x] =
+                        __float2bfloat16_rn(some ? col[threadIdx.x] / sum : 0.f);
+                    if (threadIdx.x == 0) p.lse[(size_t)tok * p.n_h + h] = some ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+                }
+        __syncthreads();  // (masks)
+    }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(512, 2)
+    k_paged_join(const __grid_constant__ Paged p, const __grid_constant__ PagedPlan w) {
+    static_assert(kDL == 512, "a column to a thread");
     __shared__ float wt[kPairs + 1];
     __shared__ float4 sum[3][128];
+    static_assert(sizeof(sum) == kJoinSmem, "shared memory");
     pdl_wait();
     const long long per = w.head->per;
-    const int n_split = w.head->n_split, lane = threadIdx.x & 31;
+    const int n_split = w.head->n_split, redo = w.head->redo, lane = threadIdx.x & 31;
+    const auto again = [&](int u) {  // row u & 127 of split tile u >> 7 is left to redo_rows
+        return redo && ((w.tiles[w.split[u >> 7]].redo[(u & 127) >> 5] >> (u & 31)) & 1);
+    };
     const int grp = threadIdx.x >> 7, c = threadIdx.x & 127;
     bool many = false;
     for (int t = 0; t < n_split; t++) {
@@ -741,7 +828,8 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
             const PagedTile tl = w.tiles[w.split[u >> 7]];
             const int row = u & 127, p0 = (int)(tl.start / per), n = (int)((tl.start + tl.steps - 1) / per) - p0 + 1;
             const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.hc * 128 + row - ti * p.n_h;
-            if (n <= kFew || ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
+            if (n <= kFew || ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1) || again(u))
+                continue;
             __syncthreads();
             if (threadIdx.x < n) wt[threadIdx.x] = w.part_lse[part_row(p0, threadIdx.x, row)];
             __syncthreads();
@@ -781,7 +869,8 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
         const PagedTile tl = w.tiles[w.split[u >> 7]];
         const int row = u & 127, p0 = (int)(tl.start / per), n = (int)((tl.start + tl.steps - 1) / per) - p0 + 1;
         const int ti = w.tpt > 1 || p.n_h == 128 ? row / p.n_h : 0, h = tl.hc * 128 + row - ti * p.n_h;
-        if (n > kFew || ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1)) continue;
+        if (n > kFew || ti >= min(w.tpt, tl.q_len - tl.i0) || h >= p.n_h || (ti > 0 && w.hchunks > 1) || again(u))
+            continue;
         const float mine = lane < n ? w.part_lse[part_row(p0, lane, row)] : -INFINITY;
         const bool nan = __any_sync(0xffffffffu, mine != mine);
         float m = mine;
@@ -816,6 +905,7 @@ __global__ void __launch_bounds__(512) k_paged_join(const Paged p, const PagedPl
             dst[lane + 32 * i] = make_uint2(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i].z, acc[i].w));
         if (lane == 0) p.lse[(size_t)tok * p.n_h + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+    if (redo) redo_rows<KIND>(p, w, reinterpret_cast<uint8_t *>(sum));
 }
 
 template <int KIND>
@@ -824,7 +914,10 @@ cudaError_t launch_t(const CUtensorMap &m4, const CUtensorMap &m1, const CUtenso
     cudaError_t e = cudaFuncSetAttribute(k_paged_tc<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     count_launch();
-    return launch_pdl(k_paged_tc<KIND>, dim3(2 * kPairs), dim3(threads_of(KIND)), kSmem, st, m4, m1, mq, p, w);
+    e = launch_pdl(k_paged_tc<KIND>, dim3(2 * kPairs), dim3(threads_of(KIND)), kSmem, st, m4, m1, mq, p, w);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    return launch_pdl(k_paged_join<KIND>, dim3(296), dim3(512), 0, st, p, w);
 }
 
 }  // namespace
@@ -839,11 +932,8 @@ cudaError_t launch_paged_tc(const Paged &p, const PagedPlan &w, cudaStream_t st)
         return cudaErrorInvalidValue;
     CUtensorMap mq{};
     if (!make_q_map(&mq, p, w)) return cudaErrorInvalidValue;
-    cudaError_t e = p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(m4, m1, mq, p, w, st)
-                                                : launch_t<DSPARK_CACHE_FP8>(m4, m1, mq, p, w, st);
-    if (e != cudaSuccess) return e;
-    count_launch();
-    return launch_pdl(k_paged_join, dim3(296), dim3(512), 0, st, p, w);
+    return p.kind == DSPARK_CACHE_BF16 ? launch_t<DSPARK_CACHE_BF16>(m4, m1, mq, p, w, st)
+                                       : launch_t<DSPARK_CACHE_FP8>(m4, m1, mq, p, w, st);
 }
 
 }  // namespace dspark

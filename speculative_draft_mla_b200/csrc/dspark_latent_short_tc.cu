@@ -408,10 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&pready[wg]);
                 const float ls = (l[0] + l[1]) + (l[2] + l[3]);
                 const float inv = ls > 0.f ? 1.f / ls : 0.f;
+                // of a row that sees no key, or NaN
+                const uint32_t none = ls != ls ? 0x7fff7fffu : 0u;
                 const int tok = it.q0 + (o.live ? o.i : 0);
                 __nv_bfloat16 *dst = (__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)(o.live ? o.h : 0) * p.o_hs;
                 const bool wide = ((uintptr_t)dst & 31) == 0;
-                if (o.live) p.lse[(size_t)tok * p.n_h + o.h] = ls > 0.f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
+                if (o.live) p.lse[(size_t)tok * p.n_h + o.h] = ls > 0.f ? (mx + log2f(ls)) * kLn2 : ls != ls ? ls : -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < kSlices; c++) {
                     const uint32_t g = n * kSlices + c, s = g & 1;
@@ -433,16 +435,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 8; e++) {
                                 const float a = u < 2 ? v0[16 * (u & 1) + 2 * e] : v1[16 * (u & 1) + 2 * e];
                                 const float b = u < 2 ? v0[16 * (u & 1) + 2 * e + 1] : v1[16 * (u & 1) + 2 * e + 1];
-                                x[e] = ls > 0.f ? pack_bf16x2(a * inv, b * inv) : 0u;
+                                x[e] = ls > 0.f ? pack_bf16x2(a * inv, b * inv) : none;
                             }
                             st_global_32B(reinterpret_cast<uint8_t *>(dst) + 128 * c + 32 * u, x, wide);
                         }
                     }
                 }
                 if (!ok) break;
-                // rows beside a key that is not finite and not theirs, and rows that see NaN
+                // Rows beside a key that is not finite and not theirs. (3 ms a tile at most, 32
+                // rows of 144 keys: no wait of another warp comes near its limit.)
                 __syncwarp();
-                uint32_t redo = __ballot_sync(0xffffffffu, o.live && (bad || ls != ls));
+                uint32_t redo = __ballot_sync(0xffffffffu, o.live && bad && ls == ls);
                 while (redo) {
                     const int who = __ffs(redo) - 1;
                     redo &= redo - 1;

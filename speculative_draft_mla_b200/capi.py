@@ -5,6 +5,10 @@ Every step of the attention runs in the CUDA library ``libdspark_attn.so``
 built in-tree by ``speculative_draft_mla_b200.build``. There is no fallback:
 if the library is missing or the tensors are not CUDA tensors, the calls raise.
 Function names follow the C entry points without the ``dspark_`` prefix.
+
+A call runs on the current stream of its tensors' device, or on ``stream``. Tensors that it allocates
+come from that stream's memory and stay safe to use and to drop on the current one; that the inputs are
+ready there, and live until they have been read, is the caller's part, as is waiting for ``stream``.
 """
 import ctypes
 import os
@@ -150,6 +154,20 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on stream (None: the current one). It comes from that stream's memory, so that no work of
+    the current stream can still hold it when the call writes it, and its memory is given away only after what both
+    streams have been given by the time it is dropped."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if here != stream:
+        t.record_stream(here)
+    return t
+
+
 def _check(status, where):
     if status != 0:
         raise DsparkError(status, where)
@@ -159,11 +177,11 @@ def workspace_size(prob):
     return int(load().dspark_workspace_size(ctypes.byref(prob)))
 
 
-def alloc_workspace(prob, device):
+def alloc_workspace(prob, device, stream=None):
     n = workspace_size(prob)
     if n == 0:
         raise DsparkError(2, "workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _empty(n, torch.uint8, device, stream)
 
 
 def _cuda(*ts):
@@ -189,10 +207,10 @@ def attn_fwd(q, kc, kr, v, anchors, keep, S, W, rope_base=10000.0, workspace=Non
     _cuda(q, kc, kr, v, anchors, keep)
     prob = problem_of(q, kc, kr, v, anchors, S, W, rope_base)
     if workspace is None:
-        workspace = alloc_workspace(prob, q.device)
+        workspace = alloc_workspace(prob, q.device, stream)
     if out is None:
-        o = torch.empty(q.shape[:3] + (v.shape[-1],), dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        o = _empty(q.shape[:3] + (v.shape[-1],), q.dtype, q.device, stream)
+        lse = _empty(q.shape[:3], torch.float32, q.device, stream)
     else:
         o, lse = out
     _cuda(o, lse, workspace)
@@ -209,9 +227,9 @@ def attn_bwd(q, kc, kr, v, anchors, keep, o, lse, dout, S, W, rope_base=10000.0,
     _cuda(q, kc, kr, v, anchors, keep, o, lse, dout)
     prob = problem_of(q, kc, kr, v, anchors, S, W, rope_base)
     if workspace is None:
-        workspace = alloc_workspace(prob, q.device)
+        workspace = alloc_workspace(prob, q.device, stream)
     if out is None:
-        dq, dkc, dkr, dv = (torch.empty_like(q), torch.empty_like(kc), torch.empty_like(kr), torch.empty_like(v))
+        dq, dkc, dkr, dv = (_empty(t.shape, t.dtype, t.device, stream) for t in (q, kc, kr, v))
     else:
         dq, dkc, dkr, dv = out
     _cuda(dq, dkc, dkr, dv, workspace)
@@ -229,8 +247,8 @@ def attn_fwd_noalloc(q, kc, kr, v, anchors, keep, S, W, rope_base=10000.0, out=N
     _cuda(q, kc, kr, v, anchors, keep, error_word)
     prob = problem_of(q, kc, kr, v, anchors, S, W, rope_base)
     if out is None:
-        o = torch.empty(q.shape[:3] + (v.shape[-1],), dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        o = _empty(q.shape[:3] + (v.shape[-1],), q.dtype, q.device, stream)
+        lse = _empty(q.shape[:3], torch.float32, q.device, stream)
     else:
         o, lse = out
     _cuda(o, lse)
@@ -264,8 +282,8 @@ def sample_anchors_gpu(loss_mask, N, seed, stream=None):
     if loss_mask.dtype != torch.uint8:
         raise TypeError("loss_mask must be uint8")
     B, S = loss_mask.shape
-    anchors = torch.empty(B, N, dtype=torch.int32, device=loss_mask.device)
-    keep = torch.empty(B, N, dtype=torch.uint8, device=loss_mask.device)
+    anchors = _empty((B, N), torch.int32, loss_mask.device, stream)
+    keep = _empty((B, N), torch.uint8, loss_mask.device, stream)
     _check(load().dspark_sample_anchors_gpu(_ptr(loss_mask), B, S, N, ctypes.c_uint64(seed & (2 ** 64 - 1)),
                                             _ptr(anchors), _ptr(keep), _stream(stream, loss_mask.device)),
            "dspark_sample_anchors_gpu")
@@ -283,9 +301,9 @@ def build_draft_inputs(input_ids, loss_mask, anchors, keep, mask_id=MASK_ID, str
     B, S = input_ids.shape
     N = anchors.shape[1]
     dev = input_ids.device
-    out = {k: torch.empty(B, 5 * N, dtype=torch.int32, device=dev)
+    out = {k: _empty((B, 5 * N), torch.int32, dev, stream)
            for k in ("draft_ids", "position_ids", "labels", "prev_ids")}
-    out["eval_mask"] = torch.empty(B, 5 * N, dtype=torch.uint8, device=dev)
+    out["eval_mask"] = _empty((B, 5 * N), torch.uint8, dev, stream)
     _check(load().dspark_build_draft_inputs(_ptr(input_ids), _ptr(loss_mask), B, S, N, _ptr(anchors), _ptr(keep),
                                             int(mask_id), _ptr(out["draft_ids"]), _ptr(out["position_ids"]),
                                             _ptr(out["labels"]), _ptr(out["prev_ids"]), _ptr(out["eval_mask"]),
@@ -307,10 +325,10 @@ def dspark_loss(student_logits, teacher_logits, labels, conf_logits, eval_mask, 
     R, V = student_logits.shape
     dev = student_logits.device
     if workspace is None:
-        workspace = torch.empty(int(load().dspark_loss_workspace_size(R)), dtype=torch.uint8, device=dev)
-    out = torch.empty(4, dtype=torch.float32, device=dev)
-    grad = torch.empty_like(student_logits) if with_grad else None
-    gconf = torch.empty(R, dtype=torch.float32, device=dev) if with_grad else None
+        workspace = _empty(int(load().dspark_loss_workspace_size(R)), torch.uint8, dev, stream)
+    out = _empty(4, torch.float32, dev, stream)
+    grad = _empty(student_logits.shape, student_logits.dtype, dev, stream) if with_grad else None
+    gconf = _empty(R, torch.float32, dev, stream) if with_grad else None
     _check(load().dspark_loss_fwd_bwd(R, V, _ptr(student_logits), _ptr(teacher_logits), _ptr(labels),
                                       _ptr(conf_logits), _ptr(eval_mask), float(alphas[0]), float(alphas[1]),
                                       float(alphas[2]), _ptr(out), _ptr(grad), _ptr(gconf), _ptr(workspace),
@@ -343,11 +361,11 @@ def latent_workspace_size(prob):
     return int(load().dspark_latent_workspace_size(ctypes.byref(prob)))
 
 
-def alloc_latent_workspace(prob, device):
+def alloc_latent_workspace(prob, device, stream=None):
     n = latent_workspace_size(prob)
     if n == 0:
         raise DsparkError(2, "latent_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _empty(n, torch.uint8, device, stream)
 
 
 def _same(name, t, shape, dtype, device):
@@ -409,10 +427,10 @@ def latent_attn_fwd(q, c, kr, anchors, keep, S, W, scale=LATENT_SCALE, rope_base
     prob = _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base)
     dev, rows = q.device, tuple(q.shape[:3])
     if workspace is None:
-        workspace = alloc_latent_workspace(prob, dev)
+        workspace = alloc_latent_workspace(prob, dev, stream)
     if out is None:
-        o = torch.empty(rows + (prob.d_l,), dtype=q.dtype, device=dev)
-        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+        o = _empty(rows + (prob.d_l,), q.dtype, dev, stream)
+        lse = _empty(rows, torch.float32, dev, stream)
     else:
         o, lse = out
         _same("o", o, rows + (prob.d_l,), q.dtype, dev)
@@ -430,11 +448,11 @@ def latent_attn_bwd(q, c, kr, anchors, keep, lse, dout, S, W, scale=LATENT_SCALE
     prob = _latent_args(q, c, kr, anchors, keep, S, W, scale, rope_base)
     dev, rows = q.device, tuple(q.shape[:3])
     if workspace is None:
-        workspace = alloc_latent_workspace(prob, dev)
+        workspace = alloc_latent_workspace(prob, dev, stream)
     _same("lse", lse, rows, torch.float32, dev)
     _same("dout", dout, rows + (prob.d_l,), q.dtype, dev)
     if out is None:
-        dq, dc, dkr = torch.empty_like(q), torch.empty_like(c), torch.empty_like(kr)
+        dq, dc, dkr = (_empty(t.shape, t.dtype, dev, stream) for t in (q, c, kr))
     else:
         dq, dc, dkr = out
         for name, g, x in (("dq", dq, q), ("dc", dc, c), ("dkr", dkr, kr)):
@@ -499,7 +517,10 @@ def latent_cache_read(cache, slots, d_l=512, d_r=64, dtype=torch.bfloat16, strea
     kind = _cache_kind(cache, d_l, d_r)
     dev, T = cache.device, slots.numel()
     _same("slots", slots, (T,), torch.int64, dev)
-    c, kr = cache.new_empty((T, d_l), dtype=dtype), cache.new_empty((T, d_r), dtype=dtype)
+    if stream is None:  # (quicker than torch.empty)
+        c, kr = cache.new_empty((T, d_l), dtype=dtype), cache.new_empty((T, d_r), dtype=dtype)
+    else:
+        c, kr = _empty((T, d_l), dtype, dev, stream), _empty((T, d_r), dtype, dev, stream)
     prob = LatentCache(T, d_l, d_r, kind, cache.shape[0], cache.shape[1], dtype_code(dtype), 0)
     _call("dspark_latent_cache_read", dev, stream, ctypes.byref(prob), _at(cache), _at(slots), _at(c), _at(kr))
     return c, kr
@@ -531,13 +552,13 @@ def latent_paged_workspace_size(prob):
     return int(load().dspark_latent_paged_workspace_size(ctypes.byref(prob)))
 
 
-def alloc_latent_paged_workspace(q, cache, block_table, max_kv_len=0, d_l=512, d_r=64, window=0):
+def alloc_latent_paged_workspace(q, cache, block_table, max_kv_len=0, d_l=512, d_r=64, window=0, stream=None):
     """Workspace of latent_attn_paged for these sizes (any mask)."""
     prob = _paged(q, cache, block_table, max_kv_len, d_l, d_r, LATENT_SCALE, True, window, 10000.0)
     n = latent_paged_workspace_size(prob)
     if n == 0:
         raise DsparkError(2, "latent_paged_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return _empty(n, torch.uint8, q.device, stream)
 
 
 def latent_attn_paged(q, cache, block_table, q_start, kv_len, max_kv_len=0, d_l=512, d_r=64, scale=LATENT_SCALE,
@@ -548,8 +569,8 @@ def latent_attn_paged(q, cache, block_table, q_start, kv_len, max_kv_len=0, d_l=
     left as they were in ``out`` and are unspecified otherwise."""
     dev, T, n_h = q.device, q.shape[0], q.shape[1]
     if out is None:
-        o = torch.empty((T, n_h, d_l), dtype=q.dtype, device=dev)
-        lse = torch.empty((T, n_h), dtype=torch.float32, device=dev)
+        o = _empty((T, n_h, d_l), q.dtype, dev, stream)
+        lse = _empty((T, n_h), torch.float32, dev, stream)
     else:
         o, lse = out
         if o.shape != (T, n_h, d_l) or o.dtype != q.dtype or o.device != dev:
@@ -563,7 +584,7 @@ def latent_attn_paged(q, cache, block_table, q_start, kv_len, max_kv_len=0, d_l=
     _same("q_start", q_start, (n_seq + 1,), torch.int32, dev)
     _same("kv_len", kv_len, (n_seq,), torch.int32, dev)
     if workspace is None:
-        workspace = torch.empty(max(latent_paged_workspace_size(prob), 256), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(latent_paged_workspace_size(prob), 256), torch.uint8, dev, stream)
     _ws_ok(workspace, dev)
     _call("dspark_latent_attn_paged", dev, stream, ctypes.byref(prob), _at(q), _at(cache), _at(block_table),
           _at(q_start), _at(kv_len), _at(o), _at(lse), _at(workspace), workspace.numel())

@@ -99,7 +99,7 @@ typedef enum { DSPARK_CACHE_F32 = 0, DSPARK_CACHE_BF16 = 1, DSPARK_CACHE_FP8 = 2
 DSPARK_API size_t dspark_latent_row_bytes(int32_t kind, int32_t d_l, int32_t d_r);
 
 typedef struct {
-    int32_t T;          /* tokens */
+    int32_t T;          /* tokens, at most 2^31 - 64 */
     int32_t d_l, d_r;   /* widths */
     int32_t kind;       /* dspark_cache_kind */
     int32_t n_pages, page_size;

@@ -97,6 +97,8 @@ dspark_status check_cache(const dspark_latent_cache *pp) {
     if (pp->kind != DSPARK_CACHE_F32 && pp->kind != DSPARK_CACHE_BF16 && pp->kind != DSPARK_CACHE_FP8)
         return DSPARK_ERR_DTYPE;
     if (pp->reserved != 0 || pp->T < 0 || pp->n_pages < 0 || pp->page_size < 1) return DSPARK_ERR_SHAPE;
+    // (the last CTA's tokens are counted past T in 32 bits)
+    if (pp->T > INT32_MAX - 63) return DSPARK_ERR_UNSUPPORTED;
     return good_widths(pp->kind, pp->d_l, pp->d_r) ? DSPARK_OK : DSPARK_ERR_UNSUPPORTED;
 }
 

@@ -433,9 +433,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         // -------------------------------------- Q -> shared and tensor memory
         uint32_t k = 0;  // segments
         bool ok = true;
+        int before = 0;  // steps of the segment before
         for (; ok && cur.next(p, w, sg); k++) {
-            if (k > 0) ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim));
+            // (the one wait that lasts as long as a segment: a limit for each 2048 steps, 5 ms)
+            if (k > 0) ok = warp_all(mbar_wait(qfree, (k - 1) & 1, abort_flag, wlim * (1 + (before >> 11))));
             if (!ok) break;
+            before = sg.s1 - sg.s0;
             ok = load_q(p, w, sg, &tm_q, sm, tmem, warp - kWarpQ, q_bytes, qland, qread, qready, k, q_issued, abort_flag, wlim);
         }
     } else if (warp == kWarpM) {

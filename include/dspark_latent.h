@@ -38,10 +38,10 @@ extern "C" {
  * The mask, anchors, keep, padding rows (O = 0, LSE = -inf, zero gradients) and
  * the check of anchors are those of dspark_attn_fwd. Every element of every
  * output is written.
- * Limits checked on the host: B >= 0, n_h >= 1, S >= 1, 0 <= N <= 8192,
- *   1 <= W <= 4096, 1 <= d_l <= 512, d_r even, 0 <= d_r <= 128,
- *   (S + 5N) * d_l < 2^31, 5N * n_h * (d_l + d_r) < 2^31, rope_base > 0,
- *   scale finite and > 0. */
+ * Limits checked on the host: 0 <= B <= 65535, n_h >= 1, 1 <= S < 2^30 - 8,
+ *   0 <= N <= 8192, 1 <= W <= 4096, 1 <= d_l <= 512, d_r even, 0 <= d_r <= 128,
+ *   (S + 5N) * max(d_l, d_r) < 2^31, 5N * n_h * (d_l + d_r) < 2^31,
+ *   B * n_h * 5N < 2^31, rope_base and scale finite and > 0. */
 typedef struct {
     int32_t B;         /* batch */
     int32_t n_h;       /* heads */
@@ -62,7 +62,7 @@ DSPARK_API size_t dspark_latent_workspace_size(const dspark_latent_problem *p);
 
 /* Forward: o and lse. flags as dspark_attn_fwd (DSPARK_FLAG_REUSE_DESCRIPTOR:
  * the workspace holds the descriptor of an earlier latent call with the same
- * anchors, keep and sizes). */
+ * anchors, keep, sizes and rope_base). */
 DSPARK_API dspark_status dspark_latent_attn_fwd(const dspark_latent_problem *p, const void *q, const void *c,
                                                 const void *kr, const int32_t *anchors, const uint8_t *keep, void *o,
                                                 float *lse, void *workspace, size_t workspace_bytes, uint32_t flags,
@@ -89,7 +89,8 @@ DSPARK_API dspark_status dspark_latent_attn_bwd(const dspark_latent_problem *p, 
  *     latent value is its e4m3 value times its scale. The scale is the least
  *     power of two 2^e, e >= -117, with |x| <= 448 * 2^e for the group's finite
  *     values (1 where they are all 0), so the values it stands for are bf16
- *     numbers; values that are not finite are stored as NaN.
+ *     numbers (but 2^128, what 248 * 2^120 and more is rounded to: infinity when
+ *     read); values that are not finite are stored as NaN.
  * Rows and caches are 16-byte aligned: d_l and d_r multiples of 8 (d_l of 128
  * for FP8). */
 typedef enum { DSPARK_CACHE_F32 = 0, DSPARK_CACHE_BF16 = 1, DSPARK_CACHE_FP8 = 2 } dspark_cache_kind;
@@ -107,9 +108,11 @@ typedef struct {
     int32_t reserved;   /* must be 0 */
 } dspark_latent_cache;
 
-/* Writes T tokens' rows: y = c * (mean(c^2) + eps)^(-1/2) * norm_weight (y = c
- * when norm_weight is NULL), the rope key turned to its position, both rounded
- * once to the cache's types, into row slots[t]. A slot outside
+/* Writes T tokens' rows into row slots[t]: y = c * (mean(c^2) + eps)^(-1/2) *
+ * norm_weight (y = c when norm_weight is NULL), rounded once to the cache's type,
+ * and the rope key turned to its position (the angle in 64 bits, sine, cosine and
+ * products in fp32: within 8 * 2^-24 of the pair's size), rounded to the cache's
+ * type of rope keys. A slot outside
  * [0, n_pages * page_size) (such as -1, a padded token) writes nothing; the
  * other slots of a call have to be distinct. Other rows stay as they were.
  *   c [T, d_l], kr [T, d_r], norm_weight [d_l] or NULL: dtype, 16-byte aligned;

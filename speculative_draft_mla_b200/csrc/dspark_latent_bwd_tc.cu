@@ -23,8 +23,9 @@
 // two slots of Q and dO a slice, and with the three that fit the copies' latency
 // is exposed: 4500 cycles a slice against 2700.)
 //
-// What bounds it (S = 4096, N = 512, B = 4, a tenth padding: 1010 us with its
-// preparation, 42000 cycles a tile): the gradients, 26000, whose 30 short products a
+// What bounds it (S = 4096, N = 512, B = 4, a tenth padding: 1090 - 1115 us with its
+// preparation where inputs change from call to call, 1010 - 1080 with the same ones, as
+// in the comparisons below; 42000 cycles a tile): the gradients, 26000, whose 30 short products a
 // slice take 1500 cycles by their shared-memory operands beside 1100 of copies in
 // and results out; S and dP, 15000, by the latency of copies that three slots
 // hide in part; the softmax between, 4400. DRAM moves little more than it must
@@ -34,7 +35,8 @@
 // may differ in the last bits before the rounding to bf16. P and dS are bf16
 // operands (an error of half a step each, as of the rounded results). The turned
 // rope slices of Q and K are hi + lo of two bf16 in S, as in the forward, and Q's
-// in its product with dS: one bf16 would nearly double the error of dkr.
+// in its product with dS: one bf16 would nearly double the error of dkr. The rope
+// part of dq is formed with the keys' hi alone, one rounding more than its latent part.
 //
 // TMEM: S 0..143 (then dS, bf16), dP 144..287, dq 288..351, dk 352..415 / 416..479, dd 480..511.
 // Warps 0-7 softmax (warps w and w + 4 share 32 rows, 64 context keys each);

@@ -11,8 +11,9 @@
 //
 // What bounds it is the stream of Q in (1152 B a row) and O out (1024 B a row):
 // at S = 8192, N = 512, B = 2 they are 0.71 GB of the 0.74 GB that have to move,
-// 113 us at the measured copy rate, against 58 us of tensor work; measured 177 us
-// (S = 2048, N = 128, B = 1: 35.5, of which 32 are one round of 2 or 3 tiles). So Q comes
+// 113 us at the measured copy rate, against 58 us of tensor work; measured 207 us with
+// inputs that change from call to call, 177 with the same ones (S = 2048, N = 128, B = 1:
+// 35.5, of which 32 are one round of 2 or 3 tiles). So Q comes
 // in 64-column slices through a ring of three, feeding S = Q K^T slice by
 // slice, and O leaves in eight 64-column products P V through two accumulators;
 // S is double-buffered, so the loads of one tile go on while the tile before it
@@ -20,7 +21,8 @@
 //
 // RoPE: the turned slices of queries and keys are split as hi + lo of two bf16
 // each and their product formed as hi hi + lo hi + hi lo, which keeps the scores
-// and the fp32 LSE to 2^-16 (one bf16 each would leave 2^-8 of the rope part).
+// and the fp32 LSE to 2^-16 (one bf16 each would leave 2^-8 of the rope part). P is
+// rounded once to bf16 as an operand: 2^-8 of each weight, as of the rounded O.
 //
 // TMEM: S 0..143 / 144..287 (P, bf16, over its own S columns), rope query hi, lo
 // 288..351, O 352..415 / 416..479.

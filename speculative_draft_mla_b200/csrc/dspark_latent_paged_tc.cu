@@ -27,14 +27,15 @@
 // the other four once O is.
 //
 // What bounds it: long contexts (16 sequences of 6 tokens over up to 16384 keys,
-// 244 us), the issue and the tensor work of a step, 3000 of its 4000 cycles (40
+// 243 us), the issue and the tensor work of a step, 3000 of its 4000 cycles (40
 // products of 64 keys, 50 cycles each where nothing else runs, 4 of 256 columns,
 // 134; issued by one lane, 268 us), and the way from S to the softmax and
 // back; few keys, the latency of the launches, of Q and of a step (one token over
-// 8192 keys, 33 us: plan 6, this kernel 13, join 8).
+// 8192 keys, 32.5 us: plan 6, this kernel 13, join 8).
 //
 // The query's turned rope slice is split as hi + lo of two bf16 (the cache's
-// rope keys are exact bf16 operands), so scores and LSE keep 2^-16.
+// rope keys are exact bf16 operands), so scores and LSE keep 2^-16. P is rounded once
+// to bf16 as an operand (2^-8 of each weight, as of the rounded O).
 //
 // TMEM: O 0..255, S 256..319, Q 320..511 (latent slices 0 - 3, rope hi, rope
 // lo). Shared: Q slices 4 - 7, two key stages, P.

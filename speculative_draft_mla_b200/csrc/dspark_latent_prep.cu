@@ -15,16 +15,6 @@ template <typename T> struct Pair;
 template <> struct Pair<float> { using V = float2; };
 template <> struct Pair<__nv_bfloat16> { using V = __nv_bfloat162; };
 
-// Position key of batch row b: context c -> c, draft key S + 5n + i -> A_n + i
-// (positions of padding or invalid blocks are clamped into the table; those
-// keys are never attended). Warp w takes positions 4 w .. 4 w + 3, lane i pairs
-// i, i + 32, ....
-//   f32: the turned keys in fp32 (CUDA-core kernels);
-//   hi, lo: x = hi + lo to 2^-17, both bf16, for the tensor cores: with one
-//   bf16 the scores would be off by up to 2^-8 of their rope part, and the fp32
-//   LSE with them; with three products hi hi + lo hi + hi lo it keeps 2^-16.
-// The warps also go over the blocks and write the padding ones' rows, and, before a
-// backward, turn the queries' rope slices and clear the accumulators.
 // The queries' rope slices turned to their positions, hi then lo, and the key
 // gradients' accumulators cleared: 313 MB at S = 4096, N = 512, B = 4, 48 us at the
 // measured copy rate, beside 76 MB of padding rows (in a launch of its own after the
@@ -57,6 +47,17 @@ __device__ __forceinline__ void bwd_rows(const BwdPrep &w, const int32_t *__rest
 }
 
 constexpr int kPadHeads = 8;
+
+// Position key of batch row b: context c -> c, draft key S + 5n + i -> A_n + i
+// (positions of padding or invalid blocks are clamped into the table; those
+// keys are never attended). Warp w takes positions 4 w .. 4 w + 3, lane i pairs
+// i, i + 32, ....
+//   f32: the turned keys in fp32 (CUDA-core kernels);
+//   hi, lo: x = hi + lo to 2^-17, both bf16, for the tensor cores: with one
+//   bf16 the scores would be off by up to 2^-8 of their rope part, and the fp32
+//   LSE with them; with three products hi hi + lo hi + hi lo it keeps 2^-16.
+// The warps also go over the blocks and write the padding ones' rows, and, before a
+// backward, turn the queries' rope slices and clear the accumulators.
 template <typename T>
 __global__ void __launch_bounds__(256) k_lat_prep(const T *__restrict__ kr, const int32_t *__restrict__ anchors,
                                                   const uint8_t *__restrict__ keep, const float2 *__restrict__ tab,

@@ -12,15 +12,17 @@
 // Item: a sequence, a chunk of 128 heads, a run of its tiles of 128 (token, head)
 // rows. Keys are gathered row by row (slots of no key are zero); 8-bit rows become
 // bf16 on the way. Q comes in 64-column slices through a ring of three. The turned
-// rope slice of the queries is hi + lo of two bf16. A row whose product met a key
+// rope slice of the queries is hi + lo of two bf16; P is rounded once to bf16 as an
+// operand (2^-8 of each weight, as of the rounded O). A row whose product met a key
 // that is not finite and not its own (0 x NaN) is evaluated again by its warp.
 //
-// 128 sequences of 5 tokens, 64 heads, window 128, 8-bit rows: 44 us, one item to an
-// SM, so that the latency of the keys and of the first tile is in the open, and that
+// 128 sequences of 5 tokens, 64 heads, window 128, 8-bit rows: 43 us of the call's 50, one
+// item to an SM, so that the latency of the keys and of the first tile is in the open, and that
 // of code not yet in the instruction cache: loops over keys that were unrolled more
 // made it 60.
-// What bounds it beyond: Q in (1152 B a row) and O out (1024 B); per tile 36 products of
-// 144 keys (80 cycles) and 72 of 64 columns (50).
+// What bounds it beyond: Q in (1152 B a row) and O out (1024 B); per tile 40 products of
+// 144 keys (80 cycles; 32 of the latents, 8 of the rope slice's hi and lo) and 72 of 64
+// columns (50).
 //
 // TMEM: S 0..143 / 144..287 (P over its own S columns), rope query hi, lo
 // 288..351, O 352..415 / 416..479.

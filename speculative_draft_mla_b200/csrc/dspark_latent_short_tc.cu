@@ -14,7 +14,8 @@
 // bf16 on the way. Q comes in 64-column slices through a ring of three. The turned
 // rope slice of the queries is hi + lo of two bf16; P is rounded once to bf16 as an
 // operand (2^-8 of each weight, as of the rounded O). A row whose product met a key
-// that is not finite and not its own (0 x NaN) is evaluated again by its warp.
+// that is not finite and not its own (0 x NaN) is evaluated again by its warp, over
+// the keys in shared memory.
 //
 // 128 sequences of 5 tokens, 64 heads, window 128, 8-bit rows: 43 us of the call's 50, one
 // item to an SM, so that the latency of the keys and of the first tile is in the open, and that
@@ -92,9 +93,99 @@ __device__ __forceinline__ uint32_t fp8x2_bf16(uint32_t w, float s) {
     return pack_bf16x2(f.x * s, f.y * s);
 }
 
+// A row once more, by a warp, over the keys in shared memory that it sees (slots
+// [lo, hi)): its product met a key that is not finite and not its own. Lane l takes
+// the scores of keys l, l + 32, .., then 16 columns of O. 32 rows over 128 keys,
+// 0.75 ms; from the cache, a key at a time, 4.2 (8-bit rows: 16).
+__device__ __noinline__ void redo_row(const Paged &p, const PagedPlan &w, const Item &it, const uint8_t *sm,
+                                      const volatile uint32_t *kmask, int i, int h, int lo, int hi) {
+    constexpr int kPer = (kKeys + 31) / 32;
+    const int lane = threadIdx.x & 31, tok = it.q0 + i;
+    const uint4 *q =
+        reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + (long long)tok * p.q_ts + (long long)h * p.q_hs);
+    const float4 *tab = reinterpret_cast<const float4 *>(w.tab + (size_t)tok * 32);
+    const auto pair = [](uint32_t x) { return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); };
+    float s[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; j++) s[j] = 0.f;
+#pragma unroll 1
+    for (int u = 0; u < (kDL + kDR) / 8; u++) {
+        const uint4 x = __ldg(q + u);
+        float2 v[4] = {pair(x.x), pair(x.y), pair(x.z), pair(x.w)};
+        if (u >= kDL / 8) {
+            const float4 c0 = __ldg(tab + 2 * (u - kDL / 8)), c1 = __ldg(tab + 2 * (u - kDL / 8) + 1);
+            const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                v[e] = make_float2(v[e].x * cs[e].x - v[e].y * cs[e].y, v[e].x * cs[e].y + v[e].y * cs[e].x);
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; j++) {
+            const int slot = min(lane + 32 * j, kKeys - 1);
+            const uint4 k = *reinterpret_cast<const uint4 *>(sm + (u >> 3) * kKSlice + sw128(slot, u & 7));
+            const float2 c[4] = {pair(k.x), pair(k.y), pair(k.z), pair(k.w)};
+#pragma unroll
+            for (int e = 0; e < 4; e++) s[j] = fmaf(v[e].x, c[e].x, fmaf(v[e].y, c[e].y, s[j]));
+        }
+    }
+    uint32_t in[kPer];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; j++) {
+        in[j] = slot_mask(lo - 32 * j, hi - 32 * j) & kmask[j];
+        s[j] *= p.scale_log2;
+        if ((in[j] >> lane) & 1) m = fmaxf(m, s[j]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float mu = m == -INFINITY ? 0.f : m;  // (scores of -inf only)
+#pragma unroll
+    for (int j = 0; j < kPer; j++) {
+        s[j] = (in[j] >> lane) & 1 ? ex2(s[j] - mu) : 0.f;
+        l += s[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    if (lane == 0) p.lse[(size_t)tok * p.n_h + h] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    // columns 8 lane .., 256 + 8 lane ..
+    float2 acc[2][4];
+#pragma unroll
+    for (int y = 0; y < 2; y++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[y][e] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kPer; j++)
+#pragma unroll 1
+        for (uint32_t x = in[j]; x; x &= x - 1) {
+            const int k = __ffs(x) - 1;
+            const float f = __shfl_sync(0xffffffffu, s[j], k);
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+                const uint4 c = *reinterpret_cast<const uint4 *>(sm + (4 * y + (lane >> 3)) * kKSlice +
+                                                                 sw128(32 * j + k, lane & 7));
+                const float2 v[4] = {pair(c.x), pair(c.y), pair(c.z), pair(c.w)};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    acc[y][e].x = fmaf(f, v[e].x, acc[y][e].x);
+                    acc[y][e].y = fmaf(f, v[e].y, acc[y][e].y);
+                }
+            }
+        }
+    __nv_bfloat16 *out = (__nv_bfloat16 *)p.o + (long long)tok * p.o_ts + (long long)h * p.o_hs;
+#pragma unroll
+    for (int y = 0; y < 2; y++) {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[e] = l != 0.f ? pack_bf16x2(acc[y][e].x * inv, acc[y][e].y * inv) : 0u;
+        reinterpret_cast<uint4 *>(out)[lane + 32 * y] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+}
+
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_short_tc(const __grid_constant__ CUtensorMap tm_q, const Paged p, const PagedPlan w, const int parts) {
+    k_short_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Paged p,
+               const __grid_constant__ PagedPlan w, const int parts) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + oBar), *kempty = kfull + 1;
@@ -109,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(kfull, kLoaders);
-        mbar_init(kempty, 1);
+        mbar_init(kempty, 1 + kWarpA);  // the last product of O, the softmax warps
         for (int i = 0; i < 2 * kQSlots; i++) mbar_init(&qfull[i], 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(&sfull[i], 1);
@@ -354,11 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------- softmax and output
         const int wg = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16), tS = trow + kColS + wg * kKeys;
-        uint32_t n = 0;
+        uint32_t n = 0, k = 0;  // tiles, items
         bool ok = true;
-        for (int i = blockIdx.x; ok && item_at(p, w, parts, i, it); i += G)
+        for (int i = blockIdx.x; ok && item_at(p, w, parts, i, it); i += G) {
+            if (it.t0 == it.t1) continue;
+            // The keys stay until every warp has seen that it needs them for no row again: at its
+            // last tile of the item, or here, where the only one is the other warps' (then after the
+            // item before: an arrival must not count for that one).
+            if (it.t1 - it.t0 == 1 && (int)(n & 1) != wg) {
+                if (k > 0) ok = warp_all(mbar_wait(kempty, (k - 1) & 1, abort_flag, wlim));
+                if (ok && lane == 0) mbar_arrive(kempty);
+            }
+            k++;
             for (int t = it.t0; ok && t < it.t1; t++, n++) {
                 if ((int)(n & 1) != wg) continue;
+                const bool last = t + 2 >= it.t1;  // of this warp's tiles of the item
                 const RowOf o(p, w, it, t, r);
                 const SeqView v{it.q0, it.q_len, it.kv, false};
                 int lo = 0, hi = 0;
@@ -366,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = warp_all(mbar_wait(&sfull[wg], (n >> 1) & 1, abort_flag, wlim));
                 if (!ok) break;
                 tc_fence_after();
-                bool bad = false;
+                float far = 0.f;  // of keys that the row does not see: 0, or NaN (0 x NaN, 0 x infinity)
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 for (int c = 0; c < it.ncol; c += 16) {
                     float s[16];
@@ -380,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; e++) {
                             const bool mine = (in >> e) & 1;
-                            bad |= !mine && !(fabsf(s[e]) < INFINITY);
+                            far = mine ? far : fmaf(0.f, s[e], far);
                             m[e & 3] = fmaxf(m[e & 3], mine ? s[e] : -INFINITY);
                         }
                     }
@@ -409,6 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pready[wg]);
                 const float ls = (l[0] + l[1]) + (l[2] + l[3]);
+                // rows beside a key that is not finite and not theirs
+                const uint32_t redo = __ballot_sync(0xffffffffu, o.live && far != 0.f && ls == ls);
+                if (last && !redo && lane == 0) mbar_arrive(kempty);
                 const float inv = ls > 0.f ? 1.f / ls : 0.f;
                 // of a row that sees no key, or NaN
                 const uint32_t none = ls != ls ? 0x7fff7fffu : 0u;
@@ -444,28 +548,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                // Rows beside a key that is not finite and not theirs. (3 ms a tile at most, 32
-                // rows of 144 keys: no wait of another warp comes near its limit.)
-                __syncwarp();
-                uint32_t redo = __ballot_sync(0xffffffffu, o.live && bad && ls == ls);
-                while (redo) {
-                    const int who = __ffs(redo) - 1;
-                    redo &= redo - 1;
-                    const int ri = __shfl_sync(0xffffffffu, o.i, who), rh = __shfl_sync(0xffffffffu, o.h, who);
-                    const int ka = __shfl_sync(0xffffffffu, lo, who), kb = __shfl_sync(0xffffffffu, hi, who);
-                    const int rtok = it.q0 + ri;
-                    float acc[18], rm, rl;
-                    paged_row<__nv_bfloat16, KIND, 18, 1>(
-                        p, it.seq, (const __nv_bfloat16 *)p.q + (long long)rtok * p.q_ts + (long long)rh * p.q_hs,
-                        it.kv - it.q_len + ri, ka, kb, acc, rm, rl);
-                    const float rinv = rl != 0.f ? 1.f / rl : 0.f;
-                    __nv_bfloat16 *out = (__nv_bfloat16 *)p.o + (long long)rtok * p.o_ts + (long long)rh * p.o_hs;
-#pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        out[lane + 32 * e] = __float2bfloat16_rn(rl != 0.f ? acc[e] * rinv : 0.f);
-                    if (lane == 0) p.lse[(size_t)rtok * p.n_h + rh] = rl != 0.f ? (rm + log2f(rl)) * kLn2 : -INFINITY;
+                if (redo) {
+                    // (the keys have long landed: for their writers' view of shared memory)
+                    ok = warp_all(mbar_wait(kfull, (k - 1) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    for (uint32_t rows = redo; rows; rows &= rows - 1) {
+                        const int who = __ffs(rows) - 1;
+                        redo_row(p, w, it, sm, kmask, __shfl_sync(0xffffffffu, o.i, who), __shfl_sync(0xffffffffu, o.h, who),
+                                 __shfl_sync(0xffffffffu, lo, who) - it.lo, __shfl_sync(0xffffffffu, hi, who) - it.lo);
+                    }
+                    __syncwarp();
+                    if (last && lane == 0) mbar_arrive(kempty);
                 }
             }
+        }
     }
 
     // ---------------------------------------------------------- teardown

@@ -150,3 +150,38 @@ def test_a_bad_row_in_a_prompt(kind, short_waits):
                          True, 0, True)
     lp.check("o", o[near], val["o"], err["o"])
     lp.check("lse", lse[near], val["lse"], err["lse"])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("n_seq", [2, 200])
+def test_a_bad_row_in_the_short_kernel(kind, n_seq):
+    """Windows that keep sequences within 144 keys, more sequences than CTAs too: a token's own row is bad, the token
+    beside it in its tile does not see it, the later ones do. Limits of 3 ms, for calls of less than 0.1."""
+    page, n_h, q_len, window, kv_len, hit = 16, 64, 20, 100, 300, 5
+    n_pages, per = 80 + n_seq * 3, -(-kv_len // page)
+    cache, lat, rope = filled(27, kind, n_pages, page, 512, 64)
+    g = torch.Generator().manual_seed(28)
+    table = torch.randint(0, 80, (n_seq, per), generator=g, dtype=torch.int32)
+    table[:, -3:] = 80 + torch.arange(3 * n_seq, dtype=torch.int32).view(n_seq, 3)  # the new tokens' pages
+    q = torch.randn(n_seq * q_len, n_h, 576, generator=g).to(torch.bfloat16)
+    qs = torch.arange(n_seq + 1, dtype=torch.int32) * q_len
+    kv = torch.full((n_seq,), kv_len, dtype=torch.int32)
+    key = kv_len - q_len + hit
+    rows = cache.view(n_pages * page, -1)
+    spoiled = list(range(0, n_seq, 2))
+    for s in spoiled:
+        rows[int(table[s, key // page]) * page + key % page] = 0xff if kind == "fp8" else float("nan")
+    prev = capi.set_wait_limit_ns(3_000_000)
+    try:
+        o, lse, ws = capi.latent_attn_paged(q.cuda(), cache, table.cuda(), qs.cuda(), kv.cuda(), window=window)
+        capi.get_error(ws)
+    finally:
+        capi.set_wait_limit_ns(prev)
+    for s in (0, 1, n_seq - 2, n_seq - 1):
+        a = s * q_len
+        val, err = reference(q[a:a + q_len].double().numpy(), lat, rope, table[s:s + 1].numpy(), [0, q_len], [kv_len], page,
+                             capi.LATENT_SCALE, True, window, True)
+        free = hit if s in spoiled else q_len
+        lp.check("o", o[a:a + free], val["o"][:free], err["o"][:free])
+        lp.check("lse", lse[a:a + free], val["lse"][:free], err["lse"][:free])
+        assert torch.isnan(o[a + free:a + q_len]).all() and torch.isnan(lse[a + free:a + q_len]).all()

@@ -218,8 +218,9 @@ cudaError_t launch_paged(const Paged &pp, void *ws, cudaStream_t st) {
     // Sequences whose tokens see up to 144 keys together go to the short kernel
     // (calls with drafts of 5 tokens, 128 sequences, 8-bit rows: a window of 140, the
     // last that it takes, 49 us, of 141, 156; bf16 rows 48 and 117. 128 tokens over up
-    // to 144 keys each, no window: 21 us, and 47 without it; one token: 17 and 18.5). It is launched where the window or the bound of kv_len makes such
-    // sequences likely, and alone where no sequence can see more.
+    // to 144 keys each, no window: 21 us, and 47 without it; one token: 17 and 18.5).
+    // It is launched where the window or the bound of kv_len makes such sequences
+    // likely, and alone where no sequence can see more.
     const auto at_most = [](long long n) { return n <= kShortKeys; };
     const bool shorts = tc && ((p.window > 0 && at_most(p.window)) || at_most(p.max_kv)) &&
                         (long long)p.n_seq * w.hchunks < (1 << 23);
